@@ -197,7 +197,8 @@ def prepare(case, seed):
 # ------------------------------------------------------------ plain forms
 def _scales(amax):
     amax = amax.clamp_min(TINY)
-    return amax / FMAX, FMAX / amax
+    top = torch.full_like(amax, FMAX)  # a number over a tensor would be its reciprocal times the number
+    return amax / top, top / amax
 
 
 def _round_e4m3(v):
