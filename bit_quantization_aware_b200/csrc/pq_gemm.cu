@@ -74,18 +74,16 @@
 // records a device status and an abort flag that ends every role's loop,
 // waits (bounded) for its own copies and MMAs in flight, frees its TMEM and
 // returns.
-#include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <stdint.h>
 
 #include <atomic>
-#include <mutex>
 
 #include "pq.h"
 #include "pq_launches.cuh"
+#include "pq_tc.cuh"
 
 namespace pqg {
 
@@ -109,7 +107,6 @@ struct Roles {
 constexpr uint32_t kTmemCols = 512;
 constexpr int kCodesSlotBytes = 16384;
 constexpr uint32_t kCodesTx = kFeat * 128;
-constexpr uint32_t kMaxSpins = 1u << 22;
 constexpr uint32_t kOnes = 0x3F803F80u;  // two bf16 1.0
 constexpr uint32_t kOnesF4 = 0x22222222u;  // eight e2m1 1.0
 constexpr uint32_t kScaleOne = 0x7F7F7F7Fu;  // four ue8m0 1.0
@@ -119,12 +116,6 @@ constexpr int64_t kF4MaxK = int64_t{1} << 20;  // exact fp32 sums up to this k
 // Arithmetic of a launch: bf16 (kind::f16, m > 16), integer (kind::i8) or
 // packed fp4 (kind::mxf4) on the same fixed-point activations.
 enum : int { kModeBF16 = 0, kModeI8 = 1, kModeF4 = 2 };
-
-// nonzero after a bounded wait gave up (read by pq_device_status)
-__device__ int g_status = 0;
-// nonzero: every launch raises its abort flag at start, so its waits give up
-// as if their cap had been reached (pq_debug_abort_waits; tests the path)
-__device__ int g_force_abort = 0;
 
 // One matrix of a launch: its tensor maps, outputs and place in the work list.
 struct Problem {
@@ -157,18 +148,6 @@ struct GemmParams {
 };
 
 // ----------------------------------------------------------- primitives
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-// K-major, 128-byte swizzle shared-memory matrix descriptor: start >> 4,
-// leading offset 16 B (unused for this layout), stride between 8-row
-// groups 1024 B, descriptor version 1, layout type 2 (128B swizzle).
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
-    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (uint64_t{1} << 16) |
-           (uint64_t{1024 >> 4} << 32) | (uint64_t{1} << 46) | (uint64_t{2} << 61);
-}
-
 // Instruction descriptor, kind::f16: fp32 accumulator, bf16 A and B, both
 // K-major, M = 128, N = nt.
 __host__ __device__ constexpr uint32_t idesc_bf16(int nt) {
@@ -221,12 +200,6 @@ __device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_
             : "memory");
 }
 
-__device__ __forceinline__ void mma_commit(uint32_t mbar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                     mbar)
-                 : "memory");
-}
-
 // NK MMAs over one stage, each reading 32 bytes of K per row (16 bf16,
 // 32 8-bit or 64 fp4 values): A columns advance by 8, the B descriptor start
 // address by 32 B inside a 128-B swizzle atom and by one atom (ATOM_B bytes)
@@ -240,79 +213,6 @@ __device__ __forceinline__ void issue_stage(uint32_t d, uint32_t a, uint64_t b0,
                      idesc, kk == 0 ? acc0 : 1u, sf);
 }
 
-__device__ __forceinline__ void mbar_init(uint32_t mbar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(mbar), "r"(count) : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive(uint32_t mbar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(mbar) : "memory");
-}
-
-__device__ __forceinline__ void mbar_expect_tx(uint32_t mbar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(mbar), "r"(bytes)
-                 : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try(uint32_t mbar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(done)
-        : "r"(mbar), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-
-// Bounded wait for the phase of the given parity (one thread). Gives up
-// early when another role raised the abort flag; raises it (and the device
-// status) when the spin limit is reached.
-// The loop is kept to the barrier try and a periodic abort check: other
-// work in it (even a rarely executed load) measurably slowed the pipeline.
-__device__ __forceinline__ bool mbar_wait(uint32_t mbar, uint32_t parity, volatile int* abort) {
-    for (uint32_t i = 0; i < kMaxSpins; ++i) {
-        if (mbar_try(mbar, parity)) return true;
-        if ((i & 63u) == 63u && *abort) return false;
-    }
-    *abort = 1;
-    atomicExch(&g_status, 1);
-    return false;
-}
-
-// The same, taken by lane 0 for the whole warp (the result is warp-uniform,
-// so the warp stays converged for the .sync.aligned tensor-memory ops).
-__device__ __forceinline__ bool warp_wait(uint32_t mbar, uint32_t parity, volatile int* abort) {
-    int ok = 0;
-    if ((threadIdx.x & 31) == 0) ok = mbar_wait(mbar, parity, abort) ? 1 : 0;
-    return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
-}
-
-// Bounded wait that ignores the abort flag (draining on the way out).
-__device__ __forceinline__ void mbar_drain(uint32_t mbar, uint32_t parity) {
-    for (uint32_t i = 0; i < kMaxSpins; ++i)
-        if (mbar_try(mbar, parity)) return;
-    atomicExch(&g_status, 1);
-}
-
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t mbar,
-                                            int32_t x, int32_t y) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(mbar), "r"(x), "r"(y)
-        : "memory");
-}
-
-__device__ __forceinline__ void fence_async_smem() {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_before() {
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
 __device__ __forceinline__ void epi_sync() {  // the 4 epilogue warps
     asm volatile("bar.sync 1, 128;" ::: "memory");
 }
@@ -417,34 +317,6 @@ __device__ __forceinline__ void decode_word(uint32_t w, uint32_t* v) {
     v[5] = pair_of<5>(w);
     v[6] = pair_of<6>(w);
     v[7] = pair_of<7>(w);
-}
-
-// Position in a ring of N mbarrier-guarded slots: slot index and the parity
-// of its current phase. A wait on parity (phase ^ 1) passes at once on a
-// fresh barrier, so a producer's first round needs no special case.
-template <int N>
-struct Ring {
-    uint32_t idx = 0, phase = 0;
-    __device__ __forceinline__ void next() {
-        if (++idx == N) {
-            idx = 0;
-            phase ^= 1u;
-        }
-    }
-};
-
-// Bounded wait for the last min(issued, N) loads of a full-barrier ring.
-template <int N>
-__device__ __forceinline__ void drain_ring(uint32_t bar0, Ring<N> r, uint32_t issued) {
-    const uint32_t n = issued < static_cast<uint32_t>(N) ? issued : static_cast<uint32_t>(N);
-    for (uint32_t j = 0; j < n; ++j) {
-        if (r.idx == 0) {
-            r.idx = N;
-            r.phase ^= 1u;
-        }
-        --r.idx;
-        mbar_drain(bar0 + 8u * r.idx, r.phase);
-    }
 }
 
 // One piece of a CTA's range: matrix pi, row block b, code chunks [c0, c1).
@@ -1833,20 +1705,6 @@ static int64_t partial_bytes(const Plan& pl, int64_t m) {
     return (static_cast<int64_t>(pl.grid) * 2 * kFeat * m4 * 4 + 255) / 256 * 256;
 }
 
-static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult qr;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &qr) ==
-                cudaSuccess &&
-            qr == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    });
-    return fn;
-}
-
 // Argument checks of one matrix (no CUDA call).
 static pq_status_t check_problem(int64_t m, const pq_gemm_problem_t& pr) {
     if (m < 1 || m > 128 || pr.n < 1 || pr.k < kMinK || pr.k % kMinK) return PQ_ERR_INVALID_ARG;
@@ -2149,19 +2007,13 @@ pq_status_t pq_wq_gemm_batch(pq_quant_t q, int64_t m, int32_t count,
 }
 
 int pq_device_status(void) {
-    int v = 0;
-    if (cudaMemcpyFromSymbol(&v, g_status, sizeof(int)) != cudaSuccess) return PQ_ERR_CUDA;
-    if (v) {
-        const int zero = 0;
-        cudaMemcpyToSymbol(g_status, &zero, sizeof(int));
-        return PQ_ERR_TIMEOUT;
-    }
-    return PQ_OK;
+    const int weight_only = take_status(), fp8 = fp8_take_status();
+    if (weight_only == PQ_ERR_CUDA || fp8 == PQ_ERR_CUDA) return PQ_ERR_CUDA;
+    return weight_only != PQ_OK ? weight_only : fp8;
 }
 
 pq_status_t pq_debug_abort_waits(int on) {
-    const int v = on ? 1 : 0;
-    return cudaMemcpyToSymbol(g_force_abort, &v, sizeof(v)) == cudaSuccess ? PQ_OK : PQ_ERR_CUDA;
+    return set_abort_waits(on) == PQ_OK && fp8_set_abort_waits(on) == PQ_OK ? PQ_OK : PQ_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -1,0 +1,87 @@
+"""The three products of a linear layer's training step in block-scaled e4m3.
+
+Around the weight quantizer, a step of one layer y = x Wq^T multiplies three
+times: y from the activations and the fake-quantized weights, dx from the
+output's gradient and the weights, and the weights' upstream gradient
+dWq = dy^T x, which the quantizer's backward takes (``pq_fakequant_bwd``,
+``pq_fakequant_bwd_adamw``). ``Fp8Linear`` quantizes each operand once
+(``pq.pq_fp8_quant``: x and dy by rows and, from the same read, by columns;
+Wq in 128 x 128 tiles with its transpose) and runs the products on the tensor
+cores (``pq.pq_fp8_gemm``). It holds the codes between forward and backward
+and allocates nothing but the outputs that the caller leaves out.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import pq
+
+
+class _Operand:
+    """Codes and scales of one operand and of its transpose, for up to
+    ``rows`` x ``cols``; ``quant`` fills and returns views of the size at hand."""
+
+    def __init__(self, block, rows, cols, device):
+        self.block, self.rows, self.cols = block, rows, cols
+        self.q = pq.fp8_empty(rows, cols, device)
+        self.qt = pq.fp8_empty(cols, rows, device)
+        count = lambda r, c: torch.Size(pq.fp8_scale_shape(block, r, c)).numel()
+        self.s = torch.empty(count(rows, cols), dtype=torch.float32, device=device)
+        self.st = torch.empty(count(cols, rows), dtype=torch.float32, device=device)
+
+    def quant(self, x, stream):
+        r, c = x.shape
+        shape, shape_t = pq.fp8_scale_shape(self.block, r, c), pq.fp8_scale_shape(self.block, c, r)
+        q, qt = self.q[:r], self.qt[:, :r]
+        s = self.s[:shape[0] * shape[1]].view(shape)
+        st = self.st[:shape_t[0] * shape_t[1]].view(shape_t)
+        pq.pq_fp8_quant(self.block, x, q, s, qt, st, stream)
+        return (q, s), (qt, st)
+
+
+class Fp8Linear:
+    """One linear layer of ``out_features`` x ``in_features`` weights over up
+    to ``max_tokens`` tokens a step."""
+
+    def __init__(self, out_features, in_features, max_tokens, device="cuda"):
+        if min(out_features, in_features, max_tokens) < 1:
+            raise ValueError("Fp8Linear: sizes must be positive")
+        self.n, self.k, self.max_tokens = int(out_features), int(in_features), int(max_tokens)
+        dev = torch.device(device)
+        self._w = _Operand(pq.PQ_BLOCK_TILE, self.n, self.k, dev)
+        self._x = _Operand(pq.PQ_BLOCK_ROW, self.max_tokens, self.k, dev)
+        self._dy = _Operand(pq.PQ_BLOCK_ROW, self.max_tokens, self.n, dev)
+        self._saved = None  # (tokens, W^T codes, x^T codes) of the last forward
+
+    def _check(self, t, rows, cols, name):
+        if t.dim() != 2 or tuple(t.shape) != (rows, cols):
+            raise ValueError(f"Fp8Linear: {name} must be [{rows}, {cols}], got {list(t.shape)}")
+
+    def forward(self, x, wq, y_out=None, stream=None):
+        """y = x Wq^T (bf16 [tokens, out_features], or ``y_out``'s type) from x
+        [tokens, in_features] and wq [out_features, in_features]."""
+        m = x.shape[0]
+        if not 1 <= m <= self.max_tokens:
+            raise ValueError(f"Fp8Linear: 1 to {self.max_tokens} tokens, got {m}")
+        self._check(x, m, self.k, "x")
+        self._check(wq, self.n, self.k, "wq")
+        w, wt = self._w.quant(wq, stream)
+        xr, xt = self._x.quant(x, stream)
+        y = y_out if y_out is not None else torch.empty((m, self.n), dtype=torch.bfloat16, device=x.device)
+        pq.pq_fp8_gemm(*xr, *w, pq.PQ_BLOCK_TILE, y, stream)
+        self._saved = (m, wt, xt)
+        return y
+
+    def backward(self, dy, dx_out=None, dw_out=None, stream=None):
+        """(dx [tokens, in_features], dWq [out_features, in_features]) of the
+        last forward, bf16 unless given, from dy [tokens, out_features]."""
+        if self._saved is None:
+            raise ValueError("Fp8Linear: backward needs a forward first")
+        m, wt, xt = self._saved
+        self._check(dy, m, self.n, "dy")
+        dyr, dyt = self._dy.quant(dy, stream)
+        dx = dx_out if dx_out is not None else torch.empty((m, self.k), dtype=torch.bfloat16, device=dy.device)
+        dw = dw_out if dw_out is not None else torch.empty((self.n, self.k), dtype=torch.bfloat16, device=dy.device)
+        pq.pq_fp8_gemm(*dyr, *wt, pq.PQ_BLOCK_TILE, dx, stream)
+        pq.pq_fp8_gemm(*dyt, *xt, pq.PQ_BLOCK_ROW, dw, stream)
+        return dx, dw

@@ -25,6 +25,9 @@ PQ_BINARY, PQ_TERNARY, PQ_SEQ2, PQ_SEQ2_B, PQ_LSQ2, PQ_LSQ3, PQ_LSQ4 = range(1, 
 QUANTIZERS = {"binary": PQ_BINARY, "ternary": PQ_TERNARY, "seq2": PQ_SEQ2,
               "seq2_b": PQ_SEQ2_B, "lsq2": PQ_LSQ2, "lsq3": PQ_LSQ3,
               "lsq4": PQ_LSQ4}
+PQ_BF16, PQ_FP16, PQ_FP32 = range(1, 4)  # pq_dtype_t
+DTYPES = {torch.bfloat16: PQ_BF16, torch.float16: PQ_FP16, torch.float32: PQ_FP32}
+PQ_BLOCK_ROW, PQ_BLOCK_TILE = 1, 2  # pq_block_t
 PQ_OK, PQ_ERR_INVALID_ARG, PQ_ERR_UNSUPPORTED, PQ_ERR_MISALIGNED, \
     PQ_ERR_CUDA, PQ_ERR_TIMEOUT = range(6)
 
@@ -84,6 +87,13 @@ class PQGemmProblem(ctypes.Structure):
                 ("alpha", ctypes.c_void_p), ("y_bf16", ctypes.c_void_p)]
 
 
+class PQTensor(ctypes.Structure):
+    """``pq_tensor_t``: one gradient tensor (device pointers)."""
+    _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32)]
+
+
 class PQIpcHandle(ctypes.Structure):
     """``pq_ipc_handle_t``: a CUDA IPC handle of one device allocation."""
     _fields_ = [("bytes", ctypes.c_ubyte * 64)]
@@ -91,6 +101,7 @@ class PQIpcHandle(ctypes.Structure):
 
 def _declare(L):
     i64, p, i32, f32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+    f64 = ctypes.c_double
     L.pq_fakequant_fwd_batch.argtypes = [i32, i32, ctypes.POINTER(PQMatrix), p]
     L.pq_fakequant_fwd_batch.restype = i32
     L.pq_fakequant_bwd_batch.argtypes = [i32, i32, ctypes.POINTER(PQMatrix), p]
@@ -102,6 +113,32 @@ def _declare(L):
                                       ctypes.POINTER(PQShard), ctypes.POINTER(PQAdamW),
                                       ctypes.POINTER(PQAdamW), p]
     L.pq_reduce_bwd_adamw.restype = i32
+    L.pq_fakequant_bwd_adamw_clip.argtypes = [i32, i32, ctypes.POINTER(PQAdamWMatrix),
+                                              ctypes.POINTER(PQAdamW), ctypes.POINTER(PQAdamW),
+                                              p, p]
+    L.pq_fakequant_bwd_adamw_clip.restype = i32
+    L.pq_reduce_bwd_adamw_clip.argtypes = [i32, i32, ctypes.POINTER(ctypes.c_void_p), f32, i32,
+                                           ctypes.POINTER(PQShard), ctypes.POINTER(PQAdamW),
+                                           ctypes.POINTER(PQAdamW), p, p]
+    L.pq_reduce_bwd_adamw_clip.restype = i32
+    L.pq_grad_norm.argtypes = [i32, ctypes.POINTER(PQTensor), i32, i32, ctypes.POINTER(PQMatrix),
+                               f64, p, p, p, p, i64, p]
+    L.pq_grad_norm.restype = i32
+    L.pq_grad_norm_workspace_bytes.argtypes = [i32, i32]
+    L.pq_grad_norm_workspace_bytes.restype = i64
+    L.pq_reduce_grad_norm.argtypes = [i32, i32, ctypes.POINTER(ctypes.c_void_p), f32, i32,
+                                      ctypes.POINTER(PQShard), f64, p, p, p, p, i64, p]
+    L.pq_reduce_grad_norm.restype = i32
+    L.pq_clip_coef.argtypes = [i32, p, f64, p, p, p]
+    L.pq_clip_coef.restype = i32
+    L.pq_grad_scale.argtypes = [i32, ctypes.POINTER(PQTensor), p, p]
+    L.pq_grad_scale.restype = i32
+    L.pq_grad_clip.argtypes = [i32, ctypes.POINTER(PQTensor), f64, p, p, p, i64, p]
+    L.pq_grad_clip.restype = i32
+    L.pq_fp8_quant.argtypes = [i32, i32, i64, i64, p, i64, p, i64, p, p, i64, p, p]
+    L.pq_fp8_quant.restype = i32
+    L.pq_fp8_gemm.argtypes = [i64, i64, i64, p, i64, p, p, i64, p, i32, p, i32, i64, p]
+    L.pq_fp8_gemm.restype = i32
     L.pq_wq_gemm.argtypes = [i32, i64, i64, i64, p, p, p, p, p, i64, p]
     L.pq_wq_gemm.restype = i32
     L.pq_wq_gemm_batch.argtypes = [i32, i64, i32, ctypes.POINTER(PQGemmProblem), p, i64, p]
@@ -289,8 +326,14 @@ def adamw(step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0):
     return PQAdamW(lr, beta1, beta2, eps, weight_decay, step)
 
 
-def pq_fakequant_bwd_adamw(q, mats, hp_w, hp_alpha, stream=None):
-    """Backward fused with one AdamW step over a ``pq_adamw_matrix_t[]``."""
+def pq_fakequant_bwd_adamw(q, mats, hp_w, hp_alpha, stream=None, coef=None):
+    """Backward fused with one AdamW step over a ``pq_adamw_matrix_t[]``;
+    ``coef`` (fp32 [1], from ``pq_grad_norm``) clips the gradients."""
+    if coef is not None:
+        _check("pq_fakequant_bwd_adamw_clip", lib().pq_fakequant_bwd_adamw_clip(
+            q, len(mats), mats, ctypes.byref(hp_w), ctypes.byref(hp_alpha), _f32_1(coef, "coef"),
+            _stream(stream)))
+        return
     _check("pq_fakequant_bwd_adamw", lib().pq_fakequant_bwd_adamw(
         q, len(mats), mats, ctypes.byref(hp_w), ctypes.byref(hp_alpha),
         _stream(stream)))
@@ -312,10 +355,17 @@ def shard_array(descs):
     return arr
 
 
-def pq_reduce_bwd_adamw(q, g_sources, grad_mult, shards, hp_w, hp_alpha, stream=None):
+def pq_reduce_bwd_adamw(q, g_sources, grad_mult, shards, hp_w, hp_alpha, stream=None,
+                        coef=None):
     """Reduce over replicas' bf16 gradients fused with backward + AdamW.
-    ``g_sources``: device pointers (ints) or CUDA tensors, one per replica."""
+    ``g_sources``: device pointers (ints) or CUDA tensors, one per replica;
+    ``coef`` (fp32 [1], from ``pq_clip_coef``) clips the gradients."""
     srcs = (ctypes.c_void_p * len(g_sources))(*[_ptr(g) for g in g_sources])
+    if coef is not None:
+        _check("pq_reduce_bwd_adamw_clip", lib().pq_reduce_bwd_adamw_clip(
+            q, len(g_sources), srcs, ctypes.c_float(grad_mult), len(shards), shards,
+            ctypes.byref(hp_w), ctypes.byref(hp_alpha), _f32_1(coef, "coef"), _stream(stream)))
+        return
     _check("pq_reduce_bwd_adamw", lib().pq_reduce_bwd_adamw(
         q, len(g_sources), srcs, ctypes.c_float(grad_mult), len(shards), shards,
         ctypes.byref(hp_w), ctypes.byref(hp_alpha), _stream(stream)))
@@ -405,6 +455,219 @@ def pq_wq_gemm_noalloc(q, x, packed, alpha, y_out, stream=None):
             raise PQError(f"pq_wq_gemm_noalloc (needs {need} B of split-K scratch, over the "
                           f"fixed {WQ_GEMM_NOALLOC_SCRATCH_BYTES} B; use pq_wq_gemm)", status)
     _check("pq_wq_gemm_noalloc", status)
+
+
+# ------------------------------------------------- gradient norm and clipping
+def _one(t, dtype, name):
+    """Pointer of a one-element device tensor (None passes as NULL)."""
+    if t is not None and (t.dtype != dtype or t.numel() != 1):
+        raise ValueError(f"{name} must be one {dtype} element on the device")
+    return _ptr(t)
+
+
+def _f32_1(t, name):
+    return _one(t, torch.float32, name)
+
+
+def _workspace(ws):
+    if ws is None:
+        return None, 0
+    return _ptr(ws), ws.numel() * ws.element_size()
+
+
+def tensor_array(tensors, outs=None):
+    """Build a ``pq_tensor_t[]`` from contiguous bf16, fp16 or fp32 CUDA
+    tensors. ``outs`` (one per tensor, or None for in place; each entry may be
+    None too) takes the scaled gradients, in the same type or fp32. A tensor
+    may be listed once only where it is scaled in place."""
+    outs = [None] * len(tensors) if outs is None else list(outs)
+    if len(outs) != len(tensors):
+        raise ValueError("outs must have one entry for each tensor")
+    arr = (PQTensor * len(tensors))()
+    written = set()
+    for d, t, o in zip(arr, tensors, outs):
+        if t.dtype not in DTYPES:
+            raise ValueError(f"gradients must be bf16, fp16 or fp32, not {t.dtype}")
+        if o is not None and (o.numel() != t.numel() or o.dtype not in (t.dtype, torch.float32)):
+            raise ValueError("an out has its tensor's size and its type or fp32")
+        d.data, d.numel, d.dtype = _ptr(t), t.numel(), DTYPES[t.dtype]
+        d.out, d.out_dtype = _ptr(o), DTYPES[o.dtype] if o is not None else 0
+        dst = d.out or d.data
+        if t.numel() and dst in written:
+            raise ValueError("two entries would write the same tensor")
+        written.add(dst)
+    return arr
+
+
+def pq_grad_norm_workspace_bytes(n_tensors, n_mats=0) -> int:
+    return int(lib().pq_grad_norm_workspace_bytes(n_tensors, n_mats))
+
+
+def pq_grad_norm(max_norm, norm_out, coef_out, workspace, tensors=None, q=0, mats=None,
+                 sumsq_out=None, stream=None):
+    """Global norm of a ``pq_tensor_t[]`` (see ``tensor_array``) and of the
+    quantizer gradients of a ``pq_matrix_t[]`` (see ``matrix_array``), and the
+    clipping factor min(1, max_norm / (norm + 1e-6)). Outputs are device
+    tensors of one element: fp32 ``norm_out``, ``coef_out``, fp64
+    ``sumsq_out``; each may be None, not all."""
+    ws, ws_bytes = _workspace(workspace)
+    _check("pq_grad_norm", lib().pq_grad_norm(
+        0 if tensors is None else len(tensors), tensors, q, 0 if mats is None else len(mats), mats,
+        max_norm, _one(sumsq_out, torch.float64, "sumsq_out"), _f32_1(norm_out, "norm_out"),
+        _f32_1(coef_out, "coef_out"), ws, ws_bytes, _stream(stream)))
+
+
+def pq_reduce_grad_norm(q, g_sources, grad_mult, shards, max_norm, norm_out, coef_out, workspace,
+                        sumsq_out=None, stream=None):
+    """``pq_grad_norm`` of row shards (see ``shard_array``), each gradient the
+    replicas' sum as in ``pq_reduce_bwd_adamw``."""
+    srcs = (ctypes.c_void_p * len(g_sources))(*[_ptr(g) for g in g_sources])
+    ws, ws_bytes = _workspace(workspace)
+    _check("pq_reduce_grad_norm", lib().pq_reduce_grad_norm(
+        q, len(g_sources), srcs, ctypes.c_float(grad_mult), len(shards), shards, max_norm,
+        _one(sumsq_out, torch.float64, "sumsq_out"), _f32_1(norm_out, "norm_out"),
+        _f32_1(coef_out, "coef_out"), ws, ws_bytes, _stream(stream)))
+
+
+def pq_clip_coef(sumsq, max_norm, norm_out, coef_out, stream=None):
+    """Norm and clipping factor from sums of squares (fp64 [count] on the
+    device), e.g. every rank's ``sumsq_out``."""
+    if sumsq.dtype != torch.float64:
+        raise ValueError("sumsq must be fp64")
+    _check("pq_clip_coef", lib().pq_clip_coef(
+        sumsq.numel(), _ptr(sumsq), max_norm, _f32_1(norm_out, "norm_out"),
+        _f32_1(coef_out, "coef_out"), _stream(stream)))
+
+
+def pq_grad_scale(tensors, coef, stream=None):
+    """Every tensor of a ``pq_tensor_t[]`` times the device factor ``coef``."""
+    _check("pq_grad_scale", lib().pq_grad_scale(
+        len(tensors), tensors, _f32_1(coef, "coef"), _stream(stream)))
+
+
+def pq_grad_clip(tensors, max_norm, norm_out, coef_out, workspace, stream=None):
+    """Clips a ``pq_tensor_t[]`` by its global norm."""
+    ws, ws_bytes = _workspace(workspace)
+    _check("pq_grad_clip", lib().pq_grad_clip(
+        len(tensors), tensors, max_norm, _f32_1(norm_out, "norm_out"),
+        _f32_1(coef_out, "coef_out"), ws, ws_bytes, _stream(stream)))
+
+
+def clip_grad_norm(tensors, max_norm, stream=None):
+    """Allocate the workspace and clip the tensors in place; returns their
+    norm before it (fp32 [1])."""
+    tensors = list(tensors)
+    if not tensors:
+        raise ValueError("clip_grad_norm needs at least one tensor")
+    dev = tensors[0].device
+    norm = torch.empty(1, dtype=torch.float32, device=dev)
+    ws = torch.empty(pq_grad_norm_workspace_bytes(len(tensors)), dtype=torch.uint8, device=dev)
+    pq_grad_clip(tensor_array(tensors), max_norm, norm, None, ws, stream)
+    return norm
+
+
+# --------------------------------------------- e4m3 blocks and their product
+def _pitch(t, name, dtypes):
+    """(pointer, row pitch in elements) of a matrix whose rows are contiguous."""
+    if t.dim() != 2 or t.dtype not in dtypes:
+        raise ValueError(f"{name} must be a matrix of {' or '.join(map(str, dtypes))}")
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    # a matrix of one row may carry any pitch
+    pitch = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    if pitch < t.shape[1]:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return t.data_ptr(), pitch
+
+
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def fp8_blocks(n) -> int:
+    """Blocks of 128 that n values take."""
+    return (n + 127) // 128
+
+
+def fp8_scale_shape(block, rows, cols):
+    """Shape of the scales of a [rows, cols] matrix: one for each 128 values
+    of a row ([blocks, rows], PQ_BLOCK_ROW) or for each 128 x 128 tile
+    ([row blocks, column blocks], PQ_BLOCK_TILE)."""
+    if block == PQ_BLOCK_ROW:
+        return fp8_blocks(cols), rows
+    if block == PQ_BLOCK_TILE:
+        return fp8_blocks(rows), fp8_blocks(cols)
+    raise ValueError("block must be PQ_BLOCK_ROW or PQ_BLOCK_TILE")
+
+
+def _scales(s, block, rows, cols, name):
+    if s.dtype != torch.float32 or tuple(s.shape) != fp8_scale_shape(block, rows, cols):
+        raise ValueError(f"{name} must be fp32 {list(fp8_scale_shape(block, rows, cols))}")
+    return _ptr(s)
+
+
+def pq_fp8_quant(block, x, q_out=None, s_out=None, qt_out=None, st_out=None, stream=None):
+    """e4m3 codes and scales of x (bf16, fp16 or fp32 [rows, cols]): ``q_out``
+    [rows, cols] with ``s_out``, and/or those of its transpose: ``qt_out``
+    [cols, rows] with ``st_out`` (shapes: ``fp8_scale_shape``)."""
+    xp, ldx = _pitch(x, "x", tuple(DTYPES))
+    rows, cols = x.shape
+    args = []
+    for q, s, r, c, name in ((q_out, s_out, rows, cols, "q_out"), (qt_out, st_out, cols, rows, "qt_out")):
+        if q is None:
+            args += [None, 0, None]
+            continue
+        if tuple(q.shape) != (r, c) or s is None:
+            raise ValueError(f"{name} must be [{r}, {c}], with its scales")
+        args += [*_pitch(q, name, _CODES), _scales(s, block, r, c, "scales of " + name)]
+    _check("pq_fp8_quant", lib().pq_fp8_quant(
+        block, DTYPES[x.dtype], rows, cols, xp, ldx, *args, _stream(stream)))
+
+
+def fp8_empty(rows, cols, device):
+    """Uninitialised e4m3 codes [rows, cols] with the row pitch that
+    ``pq_fp8_gemm`` reads (a multiple of 16 bytes)."""
+    pitch = (cols + 15) // 16 * 16
+    q = torch.empty((rows, pitch), dtype=torch.float8_e4m3fn, device=device)
+    return q if pitch == cols else q[:, :cols]
+
+
+def fp8_quant(x, block=PQ_BLOCK_ROW, transposed=False, stream=None):
+    """Allocate outputs and quantize x; returns (q, s, qt, st), the last two
+    None unless ``transposed``."""
+    rows, cols = x.shape
+    dev = x.device
+    q = fp8_empty(rows, cols, dev)
+    s = torch.empty(fp8_scale_shape(block, rows, cols), dtype=torch.float32, device=dev)
+    qt = st = None
+    if transposed:
+        qt = fp8_empty(cols, rows, dev)
+        st = torch.empty(fp8_scale_shape(block, cols, rows), dtype=torch.float32, device=dev)
+    pq_fp8_quant(block, x, q, s, qt, st, stream)
+    return q, s, qt, st
+
+
+def pq_fp8_gemm(a, a_scale, b, b_scale, b_block, y_out, stream=None):
+    """Y = A B^T of block-quantized operands: codes a [m, k] with row blocks,
+    b [n, k] with ``b_block`` blocks, y_out bf16, fp16 or fp32 [m, n]."""
+    ap, lda = _pitch(a, "a", _CODES)
+    bp, ldb = _pitch(b, "b", _CODES)
+    yp, ldy = _pitch(y_out, "y_out", tuple(DTYPES))
+    (m, k), n = a.shape, b.shape[0]
+    if b.shape[1] != k or tuple(y_out.shape) != (m, n):
+        raise ValueError("pq_fp8_gemm: shapes must be a [m, k], b [n, k], y_out [m, n]")
+    _check("pq_fp8_gemm", lib().pq_fp8_gemm(
+        m, n, k, ap, lda, _scales(a_scale, PQ_BLOCK_ROW, m, k, "a_scale"), bp, ldb,
+        _scales(b_scale, b_block, n, k, "b_scale"), b_block, yp, DTYPES[y_out.dtype], ldy,
+        _stream(stream)))
+
+
+def fp8_gemm(a, a_scale, b, b_scale, b_block=PQ_BLOCK_TILE, out_dtype=torch.bfloat16, stream=None):
+    """Allocate the output and run pq_fp8_gemm."""
+    y = torch.empty((a.shape[0], b.shape[0]), dtype=out_dtype, device=a.device)
+    pq_fp8_gemm(a, a_scale, b, b_scale, b_block, y, stream)
+    return y
 
 
 def pq_device_status() -> int:

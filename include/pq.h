@@ -263,6 +263,158 @@ PQ_API pq_status_t pq_reduce_bwd_adamw(pq_quant_t q, int32_t n_src,
                                        const pq_adamw_t* hp_w,
                                        const pq_adamw_t* hp_alpha, void* stream);
 
+/* Element types of the gradient and block-quantization calls. */
+typedef enum {
+    PQ_BF16 = 1,
+    PQ_FP16 = 2,
+    PQ_FP32 = 3
+} pq_dtype_t;
+
+/* One gradient tensor (device pointers; `numel` consecutive elements). A
+ * scaling call writes data[i] * coef, rounded once to the output's type, to
+ * `out`, or back to `data` when out is NULL. out_dtype is dtype or PQ_FP32;
+ * out overlaps no other tensor's data or out. Pointers are aligned to their
+ * element; 32-byte aligned tensors take the vector path, others an element
+ * path with the same results. Norm calls ignore out and out_dtype. */
+typedef struct {
+    void* data;
+    int64_t numel;
+    void* out;          /* nullable: in place */
+    int32_t dtype;      /* pq_dtype_t */
+    int32_t out_dtype;  /* pq_dtype_t, read when out is set */
+} pq_tensor_t;
+
+/* Global gradient norm of a training step and the clipping factor
+ *     norm = sqrt(sum g^2),   coef = min(1, max_norm / (norm + 1e-6))
+ * over n plain gradient tensors and the quantizer gradients of n_mats
+ * matrices. A matrix adds the squares of the dW and d(alpha) that
+ * pq_fakequant_bwd gives for its rows, cols, w, alpha, g_bf16 and grad_scale,
+ * formed on the fly: dW is not written (6 B read per weight, against 14 B
+ * moved by writing and rereading it), and dalpha_out receives d(alpha) when
+ * it is not NULL; other fields are ignored. `coef` then goes to
+ * pq_fakequant_bwd_adamw_clip, pq_reduce_bwd_adamw_clip or pq_grad_scale.
+ * Squares and sums are fp64 in a fixed order: the range of every type's
+ * squares is kept and the same call gives the same bits. An Inf gradient
+ * gives norm = Inf and coef = 0 (Inf * 0 = NaN where it is scaled); a NaN
+ * makes both NaN. No gradients give norm 0 and coef 1.
+ *   max_norm     >= 0; infinity gives coef 1 for every finite norm
+ *   sumsq_out    nullable double[1]: the sum of squares, e.g. one rank's
+ *                part of a sharded step (see pq_clip_coef)
+ *   norm_out     nullable float[1];   coef_out  nullable float[1]; at least
+ *                one of the three outputs is given
+ *   workspace    pq_grad_norm_workspace_bytes(n, n_mats) bytes, 16-byte
+ *                aligned, for the CTAs' partial sums; contents need no
+ *                initial value; calls that share one must not overlap
+ * tensors and mats are HOST arrays read during the call. One launch per
+ * element type (or layout) and 256 entries, and one that adds the partial
+ * sums. */
+PQ_API pq_status_t pq_grad_norm(int32_t n, const pq_tensor_t* tensors, pq_quant_t q,
+                                int32_t n_mats, const pq_matrix_t* mats, double max_norm,
+                                double* sumsq_out, float* norm_out, float* coef_out,
+                                void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of pq_grad_norm (pq_grad_clip: n_mats = 0;
+ * pq_reduce_grad_norm: n_tensors = 0), -1 for a negative count. */
+PQ_API int64_t pq_grad_norm_workspace_bytes(int32_t n_tensors, int32_t n_mats);
+
+/* pq_grad_norm over row shards: the gradient of each shard is the replicas'
+ * sum that pq_reduce_bwd_adamw would use (same arguments, same order). The
+ * sum of squares is this rank's part: gather every rank's sumsq_out and call
+ * pq_clip_coef for the factor of the whole step. */
+PQ_API pq_status_t pq_reduce_grad_norm(pq_quant_t q, int32_t n_src,
+                                       const uint16_t* const* g_sources, float grad_mult,
+                                       int32_t n, const pq_shard_t* shards, double max_norm,
+                                       double* sumsq_out, float* norm_out, float* coef_out,
+                                       void* workspace, int64_t workspace_bytes, void* stream);
+
+/* norm and coef from `count` sums of squares (DEVICE array, added in an order
+ * that count fixes): the parts of several calls or ranks. */
+PQ_API pq_status_t pq_clip_coef(int32_t count, const double* sumsq, double max_norm,
+                                float* norm_out, float* coef_out, void* stream);
+
+/* Scales n tensors by the device factor *coef (see pq_tensor_t). In-place
+ * tensors are left untouched when *coef == 1. Traffic: one read and one
+ * write of each element. */
+PQ_API pq_status_t pq_grad_scale(int32_t n, const pq_tensor_t* tensors, const float* coef,
+                                 void* stream);
+
+/* Clips n gradients by their global norm: pq_grad_norm over them, then every
+ * tensor times coef, without a launch between (the scaling kernel adds the
+ * partial sums itself). norm_out is float[1], coef_out nullable; workspace as
+ * in pq_grad_norm with n_mats = 0. The norm is that of the input. */
+PQ_API pq_status_t pq_grad_clip(int32_t n, const pq_tensor_t* tensors, double max_norm,
+                                float* norm_out, float* coef_out, void* workspace,
+                                int64_t workspace_bytes, void* stream);
+
+/* pq_fakequant_bwd_adamw and pq_reduce_bwd_adamw with clipped gradients: dW
+ * and d(alpha) are multiplied by the device factor *coef (of pq_grad_norm,
+ * pq_reduce_grad_norm or pq_clip_coef) before their AdamW step, rounded once
+ * to fp32. dalpha_out receives the unclipped d(alpha). coef is read when the
+ * kernel runs, so it may come from an earlier launch on the stream. */
+PQ_API pq_status_t pq_fakequant_bwd_adamw_clip(pq_quant_t q, int32_t n,
+                                               const pq_adamw_matrix_t* mats,
+                                               const pq_adamw_t* hp_w,
+                                               const pq_adamw_t* hp_alpha, const float* coef,
+                                               void* stream);
+PQ_API pq_status_t pq_reduce_bwd_adamw_clip(pq_quant_t q, int32_t n_src,
+                                            const uint16_t* const* g_sources, float grad_mult,
+                                            int32_t n, const pq_shard_t* shards,
+                                            const pq_adamw_t* hp_w, const pq_adamw_t* hp_alpha,
+                                            const float* coef, void* stream);
+
+/* What one scale of a block-quantized e4m3 matrix covers. */
+typedef enum {
+    PQ_BLOCK_ROW = 1,  /* 128 consecutive values of a row: scales
+                        * fp32 [ceil(cols/128)][rows] */
+    PQ_BLOCK_TILE = 2  /* a 128 x 128 tile: scales
+                        * fp32 [ceil(rows/128)][ceil(cols/128)] */
+} pq_block_t;
+
+/* Block quantization to e4m3 (8-bit floating point: 4 exponent and 3
+ * mantissa bits, largest value 448): for every block
+ *     amax = max(max |x|, 2^-96),  scale = fl(amax / 448),
+ *     code = e4m3(fl(x * fl(448 / amax)))   (nearest, ties to even, saturating)
+ * The last block of a row or column may be short. A NaN or Inf in a block
+ * makes its scale NaN or Inf, and the products that read it NaN.
+ *   dtype        type of x: PQ_BF16, PQ_FP16 or PQ_FP32
+ *   x, ldx       [rows, cols], row r at element r * ldx (ldx >= cols)
+ *   q_out, ldq, s_out     nullable together: codes [rows, cols], row r at byte
+ *                r * ldq, and their scales
+ *   qt_out, ldqt, st_out  nullable together: the same of the transpose,
+ *                codes [cols, rows] and scales of a [cols, rows] matrix (row
+ *                blocks run along x's columns), from the same read of x
+ * Bytes between a row's end and its pitch are left as they were. Fast path:
+ * x 16-byte aligned with ldx a multiple of 16 bytes, codes 8-byte aligned
+ * with pitches a multiple of 8; any other layout takes element accesses.
+ * pq_fp8_gemm wants codes 16-byte aligned and pitches a multiple of 16.
+ * Traffic: x read once, 1 B written per code. */
+PQ_API pq_status_t pq_fp8_quant(pq_block_t block, pq_dtype_t dtype, int64_t rows, int64_t cols,
+                                const void* x, int64_t ldx, uint8_t* q_out, int64_t ldq,
+                                float* s_out, uint8_t* qt_out, int64_t ldqt, float* st_out,
+                                void* stream);
+
+/* Product of two block-quantized e4m3 matrices on the tensor cores (tcgen05):
+ *   Y[m][n] = sum_kb sa(kb, m) * sb(kb, n) * sum_{k in block kb} A[m][k] * B[n][k]
+ * The sums within a block of 128 are the tensor cores' fp32 sums of exact
+ * products; they are scaled and added in fp32 in a fixed order, and rounded
+ * once to Y's type. The three products of a linear layer y = x W^T with
+ * codes of pq_fp8_quant:
+ *   y  [tokens, out] = gemm(x rows,           W tiles)
+ *   dx [tokens, in]  = gemm(dy rows,          W^T tiles)
+ *   dW [out, in]     = gemm(dy^T rows,        x^T rows)
+ *   a, lda, a_scale  codes [m, k], row r at byte r * lda, PQ_BLOCK_ROW scales
+ *   b, ldb, b_scale  codes [n, k], b_block scales
+ *   y, ldy           [m, n] of y_dtype, row r at element r * ldy, overwritten
+ * Codes are 16-byte aligned and lda, ldb multiples of 16 (TMA), else
+ * PQ_ERR_MISALIGNED; any m, n, k >= 0 (k == 0 writes zeros); Y of any
+ * alignment. Nothing is allocated and no workspace is needed. Waits inside
+ * the kernel are bounded; pq_device_status() reports one that gave up.
+ * Traffic: (m + n) k B read, m n elements written; 2 m n k flops. */
+PQ_API pq_status_t pq_fp8_gemm(int64_t m, int64_t n, int64_t k, const uint8_t* a, int64_t lda,
+                               const float* a_scale, const uint8_t* b, int64_t ldb,
+                               const float* b_scale, pq_block_t b_block, void* y,
+                               pq_dtype_t y_dtype, int64_t ldy, void* stream);
+
 /* Peer-readable buffers across processes (the row-sharded step's plumbing;
  * no counterpart in the pages, which leave multi-GPU layout to the training
  * framework). A CUDA IPC handle of the device allocation that holds a
