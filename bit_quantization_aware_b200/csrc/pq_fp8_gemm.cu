@@ -8,18 +8,26 @@
 // and added in registers by the "promote" warps while the tensor cores form
 // the next one in the other half of TMEM.
 //
-// A tile is 128 rows of A (TMEM lanes, one thread each) by NT rows of B
-// (TMEM columns). With a row on a thread, the A scale is one register, and a
-// tile scale of B another: one paired multiply-add per two elements. Row
-// scales of B are per column and come through shared memory.
+// A CTA has 128 rows of A (TMEM lanes, one promote thread each) by some rows
+// of B (TMEM columns). With a row on a thread, the A scale is one register,
+// and a tile scale of B another: one multiply-add an element. Row scales of B
+// are per column and come through shared memory.
+//
+// Large products: two CTAs (a pair) form 256 x 256 with cta_group::2, each
+// with half of B's rows in its shared memory. The columns' two halves have an
+// issuer and four promote warps each and two TMEM buffers each, so one half's
+// sums leave TMEM while the other's MMAs run: a K block passes issuer, tensor
+// cores, promote warps and back in about twice the tensor cores' time, which
+// two buffers of half the width cover and two of the whole width did not.
 //
 // Few tiles (short m and n) leave most SMs idle, so a tile's K blocks are
 // split over a cluster of SPLIT CTAs, which exchange their sums through
 // distributed shared memory and add them in rank order: no workspace, no
 // atomics, the same bits every time.
 //
-// Roles: warp 0 TMA producer, warp 1 MMA issuer, warp 2 TMEM owner and loader
-// of B's row scales, warps 4.. promote. Waits are bounded as in pq_gemm.cu.
+// Roles: warp 0 TMA producer, warps 1 and 3 MMA issuers (3 in pairs), warp 2
+// TMEM owner and loader of B's row scales, warps 4.. promote. Waits are
+// bounded as in pq_gemm.cu.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -35,96 +43,262 @@ namespace pq8 {
 
 using namespace pqg;
 
-constexpr int kBlock = 128;   // K of a scale block, and of one stage
-constexpr int kRows = 128;    // A rows of a tile
-constexpr int kScaleSlots = 4;  // K blocks of B row scales in flight
+constexpr int kBlock = 128;      // K of a scale block, and of one stage
+constexpr int kRows = 128;       // A rows of a CTA: TMEM lanes
+constexpr int kMaxStages = 16;
+constexpr int kScaleSlots = 8;   // K blocks whose B row scales are in shared memory or on their way
+constexpr int kSmemSm = 228 * 1024, kSmemCta = 1024;  // of an SM; reserved for each CTA
 
 struct Params {
-    CUtensorMap ta, tb;  // codes [m][k] in boxes of 128 B x a_box rows, [n][k] in boxes of 128 B x NT rows
+    CUtensorMap ta, tb;  // codes [m][k] in boxes of 128 B x a_bytes / 128 rows, [n][k] of 128 B x B rows
+    CUtensorMap ty;      // y in boxes of 128 B x 32 rows (tma_out)
     const float* sa;     // [kb][m]
     const float* sb;     // [n / 128][kb] (tile) or [kb][n] (row)
     void* y;
     int64_t m, n, ldy;
     int32_t kb;          // K blocks
     int32_t tiles_m, tiles_n;
-    int32_t a_bytes;     // bytes of one A box
+    int32_t a_bytes;     // of one A box
+    int32_t stages;
     int32_t dtype;       // of y
-    int32_t vec;         // 16-byte stores of whole rows are aligned
+    int32_t wide;        // 32-byte stores of rows are aligned
+    int32_t tma_out;     // y suits TMA stores
 };
 
-template <int NT, int SPLIT>
+// PAIR: two CTAs of a cluster work on one tile of 256 x NT, each with 128
+// rows of A and, of each half of the columns, half of B's rows.
+template <int NT, bool BROW, int SPLIT, bool PAIR>
 struct Layout {
-    static constexpr int kPromoteWarps = NT == 256 ? 8 : 4;
+    static constexpr int kCluster = PAIR ? 2 : SPLIT;
+    static constexpr int kHalves = PAIR ? 2 : 1;          // parts of the columns with their own issuer
+    static constexpr int kCols = NT / kHalves;            // columns of such a part, and of a promote thread
+    static constexpr int kBufs = PAIR ? 2 : 4;            // TMEM buffers of each part
+    static constexpr int kPromoteWarps = 4 * kHalves;
     static constexpr int kThreads = 128 + 32 * kPromoteWarps;
-    static constexpr int kCols = NT / (kPromoteWarps / 4);  // columns of a promote thread
-    static constexpr int kABytes = kRows * kBlock, kBBytes = NT * kBlock;
-    static constexpr int kStage = kABytes + kBBytes;
-    static constexpr int kStages = NT == 256 ? 4 : NT == 128 ? 6 : 4;
-    static constexpr uint32_t kTmemCols = 2 * NT;
-    static constexpr int kScaleOff = kStages * kStage;
-    static constexpr int kBarOff = kScaleOff + kScaleSlots * NT * 4;
-    // full, empty [stages]; dfull, dempty [2]; sfull, sempty [scale slots]; drain
-    static constexpr int kNumBars = 2 * kStages + 4 + 2 * kScaleSlots + 1;
-    static constexpr int kMiscOff = kBarOff + 8 * kNumBars;
-    static constexpr int kBytes = kMiscOff + 16 + 1024;  // + alignment slack
-    static_assert(SPLIT == 1 || kRows * NT * 4 <= kStages * kStage, "exchange fits the stages");
+    static constexpr int kBRows = kCols / (PAIR ? 2 : 1);  // B rows of a part in a CTA
+    static constexpr int kBBytes = kHalves * kBRows * kBlock;
+    static constexpr uint32_t kTmemCols = kBufs * NT;
+    static constexpr int kCtas = NT == 64 ? 2 : 1;        // resident on an SM
+    // full, empty, pair [stages]; dfull, dempty [halves x buffers]; sfull,
+    // sempty [scale slots]; drain [halves]; TMEM base, abort
+    static constexpr int kNumBars = 3 * kMaxStages + 2 * kHalves * kBufs + 2 * kScaleSlots + 2;
+    static constexpr int kMiscOff = 8 * kNumBars;
+    static constexpr int kScaleOff = 1024;
+    static constexpr int kOutOff = kScaleOff + (BROW ? kScaleSlots * NT * 4 : 0);  // PAIR: 4 KB a promote warp
+    static constexpr int kRingOff = kOutOff + (PAIR ? kPromoteWarps * 4096 : 0);
+    static_assert(kMiscOff + 8 <= kScaleOff && kOutOff % 1024 == 0, "shared memory layout");
+    // exchange of a split tile: [from rank][row][column of the slice, padded]
+    static constexpr int kSlice = NT / SPLIT, kPitch = kSlice + 4;
+    static_assert(SPLIT == 1 || (!PAIR && kSlice % 8 == 0), "slices of whole vectors");
+
+    static constexpr int kSmem = kSmemSm / kCtas - kSmemCta - 1024;  // of a CTA, less the alignment slack
+    // As many stages as fit. The MMA reads 128 rows of A whatever its box
+    // brought (the rows beyond are other stages' bytes, and lanes that are
+    // not read), so the B ring behind the A ring covers a short last box.
+    static int stages(int a_bytes) {
+        const int n = (kSmem - kRingOff) / (a_bytes + kBBytes);
+        return n < kMaxStages ? n : kMaxStages;
+    }
+    static int bytes(int a_bytes, int stages) {
+        const int ring = stages * (a_bytes + kBBytes), exchange = SPLIT > 1 ? SPLIT * kRows * kPitch * 4 : 0;
+        return kRingOff + (ring > exchange ? ring : exchange) + 1024;
+    }
+};
+
+// Position in the ring of stages (see Ring; the number of stages depends on
+// how many rows A has).
+struct StageRing {
+    uint32_t n, idx = 0, phase = 0;
+    __device__ __forceinline__ explicit StageRing(uint32_t n_) : n(n_) {}
+    __device__ __forceinline__ void next() {
+        if (++idx == n) {
+            idx = 0;
+            phase ^= 1u;
+        }
+    }
 };
 
 // Instruction descriptor, kind::f8f6f4: fp32 accumulator, e4m3 A and B, both
-// K-major, M = 128, N = nt.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int nt) {
-    return (1u << 4) | (static_cast<uint32_t>(nt >> 3) << 17) | (static_cast<uint32_t>(kRows >> 4) << 24);
+// K-major, M = m, N = nt.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int m, int nt) {
+    return (1u << 4) | (static_cast<uint32_t>(nt >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
+template <bool PAIR>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d), "l"(a), "l"(b),
+            "r"(idesc), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d), "l"(a), "l"(b),
+            "r"(idesc), "r"(acc)
+            : "memory");
+}
+
+// Arrival on a barrier (PAIR: on both CTAs' barriers) when the MMAs issued so
+// far are done.
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint32_t mbar) {
+    if constexpr (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                mbar),
+            "h"(static_cast<uint16_t>(3))
+            : "memory");
+    else
+        mma_commit(mbar);
+}
+
+// Arrival where `yes`, without a branch.
+__device__ __forceinline__ void mbar_arrive_if(uint32_t mbar, bool yes) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-        "r"(acc)
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}\n" ::"r"(mbar),
+        "r"(static_cast<uint32_t>(yes))
         : "memory");
 }
 
-// 32 columns of this warp's 32 TMEM lanes; the values are there after tmem_wait.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+// Arrival on a barrier of the cluster, without release (a release took above
+// 1000 cycles): the threads that arrive so have written no memory. They have
+// read tensor memory (tcgen05.wait::ld is over) or seen copies land, which the
+// tensor cores read where they are.
+__device__ __forceinline__ void mbar_arrive_cluster_if(uint32_t addr, bool yes) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,"
-        "%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}\n" ::"r"(addr),
+        "r"(static_cast<uint32_t>(yes))
+        : "memory");
 }
-__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// Two fp32 values in a register pair, and the paired operations on them.
-__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
-    uint64_t v;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
-    return v;
+// Whether the phase is over, for the whole warp alike. REMOTE: arrivals from
+// the other CTA, which publish no memory (see mbar_arrive_cluster).
+template <bool REMOTE>
+__device__ __forceinline__ bool mbar_try_warp(uint32_t mbar, uint32_t parity) {
+    uint32_t done;
+    if constexpr (REMOTE)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(done)
+            : "r"(mbar), "r"(parity)
+            : "memory");
+    else
+        done = mbar_try(mbar, parity);
+    return __any_sync(0xFFFFFFFFu, done);
 }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
+
+// The same asked ahead: the answer to a try takes some 100 cycles and more.
+__device__ __forceinline__ uint32_t mbar_test(uint32_t mbar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(mbar), "r"(parity)
+        : "memory");
+    return done;
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
+
+// Bounded wait of a whole warp, which stays converged and uniform. A round
+// trip between two warps over two such waits measured 175 cycles, one lane's
+// wait with a shuffle of its result 425.
+template <bool REMOTE>
+__device__ __forceinline__ bool uniform_wait(uint32_t mbar, uint32_t parity, volatile int* abort) {
+    for (uint32_t i = 0; i < kMaxSpins; ++i) {
+        if (mbar_try_warp<REMOTE>(mbar, parity)) return true;
+        if ((i & 63u) == 63u && __any_sync(0xFFFFFFFFu, *abort)) return false;
+    }
+    *abort = 1;
+    atomicExch(&g_status, 1);
+    return false;
 }
-__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
-__device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(e));
+    return e != 0;
+}
+
+// W columns of this warp's 32 TMEM lanes, a lane a thread; the values are
+// there after tmem_wait.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                   "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+                   "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+                   "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                   "=r"(r[15])
+                 : "r"(taddr));
+}
+// 32 columns of 16 TMEM lanes: thread t has lanes t / 4 (registers 4 j and
+// 4 j + 1) and t / 4 + 8 (4 j + 2 and 4 j + 3) of columns 8 j + 2 (t % 4) and
+// the one beside it.
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                   "=r"(r[15])
+                 : "r"(taddr));
+}
+// Ends this thread's reads of tensor memory; r, one of their targets, may be
+// used behind it and not before.
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15])
+                 :
+                 : "memory");
+}
 
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ void st_cluster(uint32_t a, float x, float y, float z, float w) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(x), "f"(y), "f"(z), "f"(w)
+                 : "memory");
 }
 __device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
     uint32_t a;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
     return a;
+}
+
+// Asynchronous copy of src[i] to shared memory, 0 where i >= n.
+__device__ __forceinline__ void copy4(uint32_t dst, const float* src, int64_t i, int64_t n) {
+    const bool in = i < n;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src + (in ? i : 0)),
+                 "r"(in ? 4u : 0u)
+                 : "memory");
 }
 
 // Tile t of the launch: groups of 8 row tiles walk the column tiles, so the
@@ -138,28 +312,31 @@ __device__ __forceinline__ void tile_of(const Params& p, int t, int& tm, int& tn
     tn = r / rows;
 }
 
-// Rounds v[0..N) and writes it to columns col.. of a row, N a multiple of 8.
+// Rounds v(0..N) and writes it to N columns of a row of which `left` exist.
+// WIDE: 32-byte stores, whole sectors of a thread's own row.
 template <typename T, int N, typename F>
-__device__ __forceinline__ void store_row(T* y, int64_t left, bool vec, F&& v) {
+__device__ __forceinline__ void store_row(T* y, int64_t left, bool wide, F&& v) {
+    constexpr int W = 32 / sizeof(T) < N ? 32 / sizeof(T) : N;  // elements of a store
 #pragma unroll
-    for (int c = 0; c < N; c += 8) {
-        float f[8];
+    for (int c = 0; c < N; c += W) {
+        union {
+            T e[W];
+            uint32_t w[W * sizeof(T) / 4];
+        } o;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = v(c + i);
-        if (vec && c + 8 <= left) {
-            if constexpr (sizeof(T) == 4) {
-                reinterpret_cast<float4*>(y + c)[0] = make_float4(f[0], f[1], f[2], f[3]);
-                reinterpret_cast<float4*>(y + c)[1] = make_float4(f[4], f[5], f[6], f[7]);
-            } else {
-                T h[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) h[i] = static_cast<T>(f[i]);
-                *reinterpret_cast<uint4*>(y + c) = *reinterpret_cast<const uint4*>(h);
-            }
+        for (int i = 0; i < W; ++i) o.e[i] = static_cast<T>(v(c + i));
+        if (wide && c + W <= left) {
+            if constexpr (W * sizeof(T) == 32)
+                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(y + c), "r"(o.w[0]),
+                             "r"(o.w[1]), "r"(o.w[2]), "r"(o.w[3]), "r"(o.w[4]), "r"(o.w[5]), "r"(o.w[6]),
+                             "r"(o.w[7])
+                             : "memory");
+            else
+                *reinterpret_cast<uint4*>(y + c) = make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (c + i < left) y[c + i] = static_cast<T>(f[i]);
+            for (int i = 0; i < W; ++i)
+                if (c + i < left) y[c + i] = o.e[i];
         }
     }
 }
@@ -168,231 +345,470 @@ template <int N, typename F>
 __device__ __forceinline__ void store_out(const Params& p, int64_t row, int64_t col, F&& v) {
     const int64_t left = p.n - col;
     const int64_t at = row * p.ldy + col;
-    if (p.dtype == PQ_BF16) store_row<__nv_bfloat16, N>(static_cast<__nv_bfloat16*>(p.y) + at, left, p.vec, v);
-    else if (p.dtype == PQ_FP16) store_row<__half, N>(static_cast<__half*>(p.y) + at, left, p.vec, v);
-    else store_row<float, N>(static_cast<float*>(p.y) + at, left, p.vec, v);
+    if (p.dtype == PQ_BF16) store_row<__nv_bfloat16, N>(static_cast<__nv_bfloat16*>(p.y) + at, left, p.wide, v);
+    else if (p.dtype == PQ_FP16) store_row<__half, N>(static_cast<__half*>(p.y) + at, left, p.wide, v);
+    else store_row<float, N>(static_cast<float*>(p.y) + at, left, p.wide, v);
 }
 
-template <int NT, bool BROW, int SPLIT>
-__global__ void __cluster_dims__(SPLIT, 1, 1) __launch_bounds__(Layout<NT, SPLIT>::kThreads, 1)
-    fp8_gemm_kernel(const __grid_constant__ Params p) {
-    using L = Layout<NT, SPLIT>;
-    constexpr int S = L::kStages;
+// A warp's 32 rows x N columns through its 4 KB of shared memory and the TMA
+// engine, 128 bytes of each row at a time (the 128B swizzle: 16-byte chunk c
+// of row r at chunk c ^ (r % 8), so the writes are free of bank conflicts).
+// Rows and columns beyond y are clipped. Direct stores of whole sectors a
+// thread took 5000 cycles a tile, during which no K block left TMEM.
+template <typename T, int N, typename F>
+__device__ __forceinline__ void store_tma_typed(const Params& p, uint32_t buf, int lane, int64_t row0, int64_t col,
+                                                F&& v) {
+    constexpr int W = 128 / sizeof(T);  // columns of a round
+#pragma unroll
+    for (int c = 0; c < N; c += W) {
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            union {
+                T e[16 / sizeof(T)];
+                uint32_t w[4];
+            } o;
+#pragma unroll
+            for (int i = 0; i < 16 / static_cast<int>(sizeof(T)); ++i)
+                o.e[i] = static_cast<T>(v(c + q * (16 / static_cast<int>(sizeof(T))) + i));
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             buf + lane * 128 + ((q ^ (lane & 7)) << 4)),
+                         "r"(o.w[0]), "r"(o.w[1]), "r"(o.w[2]), "r"(o.w[3])
+                         : "memory");
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0 && row0 < p.m && col + c < p.n) {
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                             reinterpret_cast<uint64_t>(&p.ty)),
+                         "r"(buf), "r"(static_cast<int32_t>(col + c)), "r"(static_cast<int32_t>(row0))
+                         : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+    }
+}
+
+template <int N, typename F>
+__device__ __forceinline__ void store_tma(const Params& p, uint32_t buf, int lane, int64_t row0, int64_t col, F&& v) {
+    if (p.dtype == PQ_BF16) store_tma_typed<__nv_bfloat16, N>(p, buf, lane, row0, col, v);
+    else if (p.dtype == PQ_FP16) store_tma_typed<__half, N>(p, buf, lane, row0, col, v);
+    else store_tma_typed<float, N>(p, buf, lane, row0, col, v);
+}
+
+template <int NT, bool BROW, int SPLIT, bool PAIR>
+__global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
+    __launch_bounds__(Layout<NT, BROW, SPLIT, PAIR>::kThreads, Layout<NT, BROW, SPLIT, PAIR>::kCtas)
+        fp8_gemm_kernel(const __grid_constant__ Params p) {
+    using L = Layout<NT, BROW, SPLIT, PAIR>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t{1023});
     const uint32_t sbase = smem_u32(smem);
-    const uint32_t b_full = sbase + L::kBarOff, b_empty = b_full + 8u * S;
-    const uint32_t b_dfull = b_empty + 8u * S, b_dempty = b_dfull + 16u;
-    const uint32_t b_sfull = b_dempty + 16u, b_sempty = b_sfull + 8u * kScaleSlots;
+    const uint32_t b_full = sbase, b_empty = b_full + 8u * kMaxStages, b_pair = b_empty + 8u * kMaxStages;
+    constexpr uint32_t kD = 8u * L::kHalves * L::kBufs;
+    const uint32_t b_dfull = b_pair + 8u * kMaxStages, b_dempty = b_dfull + kD;
+    const uint32_t b_sfull = b_dempty + kD, b_sempty = b_sfull + 8u * kScaleSlots;
     const uint32_t b_drain = b_sempty + 8u * kScaleSlots;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
     volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
-    float* bscale = reinterpret_cast<float*>(smem + L::kScaleOff);
+    const float* scales = reinterpret_cast<const float*>(smem + L::kScaleOff);
+    const uint32_t a_ring = sbase + L::kRingOff, b_ring = a_ring + p.stages * p.a_bytes;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
-        for (int s = 0; s < S; ++s) {
+        for (int s = 0; s < p.stages; ++s) {
             mbar_init(b_full + 8u * s, 1);
-            mbar_init(b_empty + 8u * s, 1);
+            mbar_init(b_empty + 8u * s, L::kHalves);
+            mbar_init(b_pair + 8u * s, 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < L::kHalves * L::kBufs; ++b) {
             mbar_init(b_dfull + 8u * b, 1);
-            mbar_init(b_dempty + 8u * b, L::kPromoteWarps);
+            mbar_init(b_dempty + 8u * b, PAIR ? 8 : 4);  // a half's promote warps, of both CTAs
         }
         for (int s = 0; s < kScaleSlots; ++s) {
             mbar_init(b_sfull + 8u * s, 32);
             mbar_init(b_sempty + 8u * s, L::kPromoteWarps);
         }
-        mbar_init(b_drain, 1);
+        for (int h = 0; h < L::kHalves; ++h) mbar_init(b_drain + 8u * h, 1);
         const int forced = *static_cast<volatile int*>(&g_force_abort);
         *abort = forced;
         if (forced) atomicExch(&g_status, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 2) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_u32(tmem_slot)),
-                     "r"(L::kTmemCols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(tmem_slot)),
+                         "r"(L::kTmemCols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(tmem_slot)),
+                         "r"(L::kTmemCols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (PAIR) cluster_sync();  // the other CTA's barriers are there
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    // this CTA's tiles, and its K blocks of each
+    // this CTA's tiles, its K blocks of each, its rows within a tile
     const int tiles = p.tiles_m * p.tiles_n;
-    const int rank = SPLIT == 1 ? 0 : static_cast<int>(blockIdx.x % SPLIT);
-    const int first = SPLIT == 1 ? blockIdx.x : blockIdx.x / SPLIT;
-    const int step = SPLIT == 1 ? gridDim.x : gridDim.x / SPLIT;
-    const int k0 = static_cast<int>(static_cast<int64_t>(p.kb) * rank / SPLIT);
-    const int k1 = static_cast<int>(static_cast<int64_t>(p.kb) * (rank + 1) / SPLIT);
+    const int rank = L::kCluster == 1 ? 0 : static_cast<int>(blockIdx.x % L::kCluster);
+    const int first = blockIdx.x / L::kCluster;
+    const int step = gridDim.x / L::kCluster;
+    const int k0 = SPLIT == 1 ? 0 : static_cast<int>(static_cast<int64_t>(p.kb) * rank / SPLIT);
+    const int k1 = SPLIT == 1 ? p.kb : static_cast<int>(static_cast<int64_t>(p.kb) * (rank + 1) / SPLIT);
+    constexpr int kTileRows = PAIR ? 2 * kRows : kRows;
+    const int row_off = PAIR ? rank * kRows : 0;
 
-    if (warp == 0) {
-        // ------------------------------------------------------ producer
-        if (lane == 0) {
-            Ring<S> r;
-            uint32_t issued = 0;
-            bool ok = true;
-            for (int t = first; ok && t < tiles; t += step) {
-                int tm, tn;
-                tile_of(p, t, tm, tn);
-                for (int kb = k0; kb < k1; ++kb) {
-                    if (!mbar_wait(b_empty + 8u * r.idx, r.phase ^ 1u, abort)) {
-                        ok = false;
-                        break;
+    // A pair's CTA launches with 168 registers a thread (64,512 in all); the
+    // promote warps' 128 sums need more: 8 x 32 x 224 + 4 x 32 x 56 = 64,512
+    constexpr bool kSplitRegs = PAIR;
+    if (warp < 4) {
+        if constexpr (kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 0) {
+            // ------------------------------------------------------ producer
+            if (lane == 0) {
+                StageRing r(p.stages);
+                int issued = 0;
+                bool ok = true;
+                for (int t = first; ok && t < tiles; t += step) {
+                    int tm, tn;
+                    tile_of(p, t, tm, tn);
+                    const int ra = tm * kTileRows + row_off, rb = tn * NT + (PAIR ? rank * L::kBRows : 0);
+                    static_assert(L::kBBytes % 1024 == 0, "swizzle atoms");
+                    for (int kb = k0; kb < k1; ++kb) {
+                        if (!mbar_wait(b_empty + 8u * r.idx, r.phase ^ 1u, abort)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t bar = b_full + 8u * r.idx;
+                        mbar_expect_tx(bar, static_cast<uint32_t>(p.a_bytes) + L::kBBytes);
+                        tma_load_2d(a_ring + r.idx * p.a_bytes, &p.ta, bar, kb * kBlock, ra);
+#pragma unroll
+                        for (int h = 0; h < L::kHalves; ++h)
+                            tma_load_2d(b_ring + r.idx * L::kBBytes + h * L::kBRows * kBlock, &p.tb, bar, kb * kBlock,
+                                        rb + h * L::kCols);
+                        r.next();
+                        if (issued < p.stages) ++issued;
                     }
-                    const uint32_t bar = b_full + 8u * r.idx, dst = sbase + r.idx * L::kStage;
-                    mbar_expect_tx(bar, static_cast<uint32_t>(p.a_bytes) + L::kBBytes);
-                    tma_load_2d(dst, &p.ta, bar, kb * kBlock, tm * kRows);
-                    tma_load_2d(dst + L::kABytes, &p.tb, bar, kb * kBlock, tn * NT);
-                    r.next();
-                    ++issued;
+                }
+                // loads in flight land before the CTA may exit
+                for (; issued > 0; --issued) {
+                    if (r.idx == 0) {
+                        r.idx = r.n;
+                        r.phase ^= 1u;
+                    }
+                    --r.idx;
+                    mbar_drain(b_full + 8u * r.idx, r.phase);
                 }
             }
-            drain_ring(b_full, r, issued);  // loads in flight land before the CTA may exit
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ---------------------------------------------------- MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_e4m3(NT);
-            Ring<S> r;
-            Ring<2> d;
-            bool ok = true;
-            for (int t = first; ok && t < tiles; t += step) {
-                for (int kb = k0; kb < k1; ++kb) {
-                    if (!mbar_wait(b_dempty + 8u * d.idx, d.phase ^ 1u, abort) ||
-                        !mbar_wait(b_full + 8u * r.idx, r.phase, abort)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t at = sbase + r.idx * L::kStage;
-                    const uint64_t a = sw128_desc(at), b = sw128_desc(at + L::kABytes);
+            __syncwarp();
+        } else if (warp == 1 || (PAIR && warp == 3 && rank == 0)) {
+            if (!PAIR || rank == 0) {
+                // ------------------------------------------------ MMA issuer
+                // The whole warp walks the loop and one lane issues: the
+                // descriptors then stay in uniform registers. Inside a branch
+                // of one lane each MMA took some 95 cycles to issue.
+                constexpr uint32_t idesc = idesc_e4m3(kTileRows, L::kCols);
+                const int h = warp == 3;
+                const uint32_t dfull = b_dfull + 8u * L::kBufs * h, dempty = b_dempty + 8u * L::kBufs * h;
+                const bool one = elect_one();
+                StageRing r(p.stages);
+                Ring<L::kBufs> d;
+                bool ok = true;
+                for (int t = first; ok && t < tiles; t += step) {
+                    for (int kb = k0; kb < k1; ++kb) {
+                        const uint64_t a = sw128_desc(a_ring + r.idx * p.a_bytes);
+                        const uint64_t b = sw128_desc(b_ring + r.idx * L::kBBytes + h * L::kBRows * kBlock);
+                        const uint32_t acc = tmem + (d.idx * L::kHalves + h) * L::kCols;
+                        const uint32_t free_bar = b_empty + 8u * r.idx, full_bar = dfull + 8u * d.idx;
+                        // operands first: they are early, the buffer is what the loop waits for
+                        if (!uniform_wait<false>(b_full + 8u * r.idx, r.phase, abort) ||
+                            (PAIR && !uniform_wait<true>(b_pair + 8u * r.idx, r.phase, abort)) ||
+                            !uniform_wait<PAIR>(dempty + 8u * d.idx, d.phase ^ 1u, abort)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (one) {
 #pragma unroll
-                    for (int k = 0; k < kBlock / 32; ++k)
-                        mma_ss(tmem + NT * d.idx, a + 2u * k, b + 2u * k, idesc, k > 0);
-                    mma_commit(b_empty + 8u * r.idx);
-                    mma_commit(b_dfull + 8u * d.idx);
-                    r.next();
-                    d.next();
+                            for (int k = 0; k < kBlock / 32; ++k)
+                                mma_ss<PAIR>(acc, a + 2u * k, b + 2u * k, idesc, k > 0);
+                            commit<PAIR>(full_bar);
+                            commit<PAIR>(free_bar);
+                        }
+                        __syncwarp();
+                        r.next();
+                        d.next();
+                    }
                 }
-            }
-            mma_commit(b_drain);  // every MMA completes before TMEM is freed
-            mbar_drain(b_drain, 0);
-        }
-        __syncwarp();
-    } else if (warp == 2) {
-        // ------------------------------------------- B's row scales
-        if constexpr (BROW) {
-            Ring<kScaleSlots> r;
-            bool ok = true;
-            for (int t = first; ok && t < tiles; t += step) {
-                int tm, tn;
-                tile_of(p, t, tm, tn);
-                for (int kb = k0; kb < k1; ++kb) {
-                    if (!warp_wait(b_sempty + 8u * r.idx, r.phase ^ 1u, abort)) {
-                        ok = false;
-                        break;
+                // every MMA completes before TMEM is freed
+                if (one) {
+                    commit<PAIR>(b_drain + 8u * h);
+                    mbar_drain(b_drain + 8u * h, 0);
+                }
+            } else {
+                // ------- the pair's other CTA: its operands are here, too
+                const uint32_t pair0 = map_to_rank(b_pair, 0);
+                const bool one = elect_one();
+                StageRing r(p.stages);
+                bool ok = true;
+                for (int t = first; ok && t < tiles; t += step)
+                    for (int kb = k0; kb < k1; ++kb) {
+                        if (!uniform_wait<false>(b_full + 8u * r.idx, r.phase, abort)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive_cluster_if(pair0 + 8u * r.idx, one);
+                        r.next();
                     }
+                if (one)  // the issuers' last arrivals here
+                    for (int h = 0; h < L::kHalves; ++h) mbar_drain(b_drain + 8u * h, 0);
+            }
+            __syncwarp();
+        } else if (warp == 2) {
+            // ------------------------------------------- B's row scales
+            if constexpr (BROW) {
+                Ring<kScaleSlots> r;
+                bool ok = true;
+                for (int t = first; ok && t < tiles; t += step) {
+                    int tm, tn;
+                    tile_of(p, t, tm, tn);
+                    for (int kb = k0; kb < k1; ++kb) {
+                        if (!warp_wait(b_sempty + 8u * r.idx, r.phase ^ 1u, abort)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t slot = sbase + L::kScaleOff + r.idx * (NT * 4);
+                        const int64_t col = static_cast<int64_t>(tn) * NT + lane;
 #pragma unroll
-                    for (int i = 0; i < NT / 32; ++i) {
-                        const int64_t col = static_cast<int64_t>(tn) * NT + 32 * i + lane;
-                        const bool in = col < p.n;
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
-                                         smem_u32(bscale + r.idx * NT + 32 * i + lane)),
-                                     "l"(p.sb + (in ? kb * p.n + col : 0)), "r"(in ? 4u : 0u)
+                        for (int i = 0; i < NT / 32; ++i)
+                            copy4(slot + 4 * (32 * i + lane), p.sb + kb * p.n, col + 32 * i, p.n);
+                        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(b_sfull + 8u * r.idx)
                                      : "memory");
+                        r.next();
                     }
-                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(b_sfull + 8u * r.idx)
-                                 : "memory");
-                    r.next();
                 }
+                asm volatile("cp.async.wait_all;" ::: "memory");
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
         }
-    } else if (warp >= 4) {
+        if constexpr (SPLIT > 1) {  // the promote warps' two barriers
+            cluster_sync();
+            cluster_sync();
+        }
+    } else {
+        if constexpr (kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         // ------------------------------------------------------- promote
         const int quarter = warp & 3, half = (warp - 4) >> 2;
         const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
         constexpr int C = L::kCols;
-        Ring<2> d;
+        const uint32_t dfull = b_dfull + 8u * L::kBufs * half;
+        const uint32_t dempty0 = b_dempty + 8u * L::kBufs * half;
+        const uint32_t dempty = PAIR ? map_to_rank(dempty0, 0) : dempty0;  // the issuer's
+        const uint32_t out_buf = sbase + L::kOutOff + (warp - 4) * 4096;
+        Ring<L::kBufs> d;
         Ring<kScaleSlots> sr;
         bool ok = true;
-        for (int t = first; ok && t < tiles; t += step) {
-            int tm, tn;
-            tile_of(p, t, tm, tn);
-            const int64_t row = static_cast<int64_t>(tm) * kRows + quarter * 32 + lane;
-            const int64_t col = static_cast<int64_t>(tn) * NT + half * C;
+        const bool one = lane == 0;
+        auto free_buffer = [&](uint32_t bar) {
+            tc_fence_before();
+            __syncwarp();
+            if constexpr (PAIR) mbar_arrive_cluster_if(bar, one);
+            else mbar_arrive_if(bar, one);
+        };
+        auto buffer = [&]() { return tmem + lane_addr + (d.idx * L::kHalves + half) * C; };
+        // The tile's K blocks into acc, tile scales: an element is one
+        // multiply-add behind a TMEM read. The reads run one chunk ahead of
+        // the arithmetic, across K blocks too; whether the next block is
+        // there is asked two chunks before. (Paired multiply-adds, f32x2,
+        // measured slower: 54 against 42 cycles a warp and 32 columns.)
+        auto sum_blocks_tile = [&](float(&acc)[C], int64_t row, int64_t col) -> bool {
+            constexpr int W = NT == 64 ? 16 : 32;  // columns of a read (registers)
+            // rows, columns and K blocks beyond the last take the last one's
+            // scale (a branch around each load took 60 cycles)
+            const float* sa = p.sa + (row < p.m ? row : p.m - 1);
+            const float* sb = p.sb + (col < p.n ? col / kBlock : (p.n - 1) / kBlock) * p.kb;
+            // scales four K blocks at a time, the next four on their way; an
+            // operation on a load, a move included, waits for it
+            float na[4], nb[4], cur[4];
+            auto fetch = [&](int g) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int b = min(g + j, k1 - 1);
+                    na[j] = __ldg(sa + b * p.m);
+                    nb[j] = __ldg(sb + b);
+                }
+            };
+            if (k0 >= k1) return true;
+            fetch(k0);
+            uint32_t v[2][W];
+            if (!uniform_wait<false>(dfull + 8u * d.idx, d.phase, abort)) return false;
+            tc_fence_after();
+            tmem_ld(buffer(), v[0]);
+            for (int kb = k0; kb < k1; ++kb) {
+                const int j = (kb - k0) & 3;
+                if (j == 0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) cur[i] = __fmul_rn(na[i], nb[i]);
+                    fetch(kb + 4);
+                }
+                const float s = j & 2 ? (j & 1 ? cur[3] : cur[2]) : (j & 1 ? cur[1] : cur[0]);
+                const uint32_t src = buffer(), free_bar = dempty + 8u * d.idx;
+                d.next();
+                uint32_t ready = 0;
+                auto add = [&](int c) {
+#pragma unroll
+                    for (int i = 0; i < W; ++i)
+                        acc[c + i] = __fmaf_rn(__uint_as_float(v[c / W % 2][i]), s, acc[c + i]);
+                };
+#pragma unroll
+                for (int c = 0; c + W < C; c += W) {
+                    tmem_wait(v[c / W % 2]);
+                    tmem_ld(src + c + W, v[(c / W + 1) % 2]);
+                    if (c + 3 * W == C) ready = mbar_test(dfull + 8u * d.idx, d.phase);
+                    add(c);
+                }
+                tmem_wait(v[(C / W - 1) % 2]);
+                free_buffer(free_bar);  // all read: the issuer may write the buffer again
+                if (kb + 1 < k1) {
+                    if (__any_sync(0xFFFFFFFFu, ready)) {
+                        tc_fence_after();
+                        tmem_ld(buffer(), v[0]);
+                        add(C - W);
+                        continue;
+                    }
+                    add(C - W);
+                    if (!uniform_wait<false>(dfull + 8u * d.idx, d.phase, abort)) return false;
+                    tc_fence_after();
+                    tmem_ld(buffer(), v[0]);
+                } else {
+                    add(C - W);
+                }
+            }
+            return true;
+        };
+        // The same with row scales of B, in shared memory: an element is a
+        // multiplication and a multiply-add.
+        auto sum_blocks_row = [&](float(&acc)[C], int64_t row, int64_t col) -> bool {
             const bool live = row < p.m;
             const float* sa = p.sa + (live ? row : 0);
-            const float* sb = p.sb + (BROW ? 0 : col / kBlock * p.kb);
-            const bool sb_in = !BROW && col < p.n;
-            uint64_t acc[C / 2];
-#pragma unroll
-            for (int i = 0; i < C / 2; ++i) acc[i] = 0;
-            // scales two K blocks ahead
-            auto scale = [&](int kb) {
-                float v = live && kb < k1 ? __ldg(sa + kb * p.m) : 0.0f;
-                if (!BROW) v = __fmul_rn(v, sb_in && kb < k1 ? __ldg(sb + kb) : 0.0f);
-                return v;
-            };
-            float s0 = scale(k0), s1 = scale(k0 + 1);
+            float next = live && k0 < k1 ? __ldg(sa + k0 * p.m) : 0.0f;
             for (int kb = k0; kb < k1; ++kb) {
-                const float s = s0;
-                s0 = s1;
-                s1 = scale(kb + 2);
-                if (BROW && !warp_wait(b_sfull + 8u * sr.idx, sr.phase, abort)) {
-                    ok = false;
-                    break;
-                }
-                if (!warp_wait(b_dfull + 8u * d.idx, d.phase, abort)) {
-                    ok = false;
-                    break;
-                }
+                const float s = next;
+                next = live && kb + 1 < k1 ? __ldg(sa + (kb + 1) * p.m) : 0.0f;
+                if (!uniform_wait<false>(b_sfull + 8u * sr.idx, sr.phase, abort) ||
+                    !uniform_wait<false>(dfull + 8u * d.idx, d.phase, abort))
+                    return false;
                 tc_fence_after();
-                const uint64_t s2 = pair(__float_as_uint(s), __float_as_uint(s));
-                const float4* bs = reinterpret_cast<const float4*>(bscale + sr.idx * NT + half * C);
+                const float4* bs = reinterpret_cast<const float4*>(scales + sr.idx * NT + half * C);
 #pragma unroll
                 for (int c = 0; c < C; c += 32) {
                     uint32_t v[32];
-                    tmem_ld32(tmem + lane_addr + NT * d.idx + half * C + c, v);
-                    tmem_wait();
+                    tmem_ld(buffer() + c, v);
+                    tmem_wait(v);
+                    if (c + 32 == C) free_buffer(dempty + 8u * d.idx);
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
-                        uint64_t f0 = s2, f1 = s2;
-                        if constexpr (BROW) {
-                            const float4 b = bs[(c + i) / 4];
-                            f0 = mul2(s2, pair(__float_as_uint(b.x), __float_as_uint(b.y)));
-                            f1 = mul2(s2, pair(__float_as_uint(b.z), __float_as_uint(b.w)));
-                        }
-                        acc[(c + i) / 2] = fma2(pair(v[i], v[i + 1]), f0, acc[(c + i) / 2]);
-                        acc[(c + i) / 2 + 1] = fma2(pair(v[i + 2], v[i + 3]), f1, acc[(c + i) / 2 + 1]);
+                        const float4 b = bs[(c + i) / 4];
+                        acc[c + i] = __fmaf_rn(__fmul_rn(__uint_as_float(v[i]), b.x), s, acc[c + i]);
+                        acc[c + i + 1] = __fmaf_rn(__fmul_rn(__uint_as_float(v[i + 1]), b.y), s, acc[c + i + 1]);
+                        acc[c + i + 2] = __fmaf_rn(__fmul_rn(__uint_as_float(v[i + 2]), b.z), s, acc[c + i + 2]);
+                        acc[c + i + 3] = __fmaf_rn(__fmul_rn(__uint_as_float(v[i + 3]), b.w), s, acc[c + i + 3]);
                     }
                 }
-                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(b_dempty + 8u * d.idx);
-                    if (BROW) mbar_arrive(b_sempty + 8u * sr.idx);
-                }
+                mbar_arrive_if(b_sempty + 8u * sr.idx, one);
+                sr.next();
                 d.next();
-                if (BROW) sr.next();
+            }
+            return true;
+        };
+        auto sum_blocks = [&](float(&acc)[C], int64_t row, int64_t col) -> bool {
+            if constexpr (BROW) return sum_blocks_row(acc, row, col);
+            else return sum_blocks_tile(acc, row, col);
+        };
+        for (int t = first; ok && t < tiles; t += step) {
+            int tm, tn;
+            tile_of(p, t, tm, tn);
+            const int64_t row = static_cast<int64_t>(tm) * kTileRows + row_off + quarter * 32 + lane;
+            const int64_t col = static_cast<int64_t>(tn) * NT + half * C;
+            const bool live = row < p.m;
+            float acc[C];
+#pragma unroll
+            for (int i = 0; i < C; ++i) acc[i] = 0.0f;
+            ok = sum_blocks(acc, row, col);
+            if constexpr (SPLIT > 1) {
+                // every CTA's stages are free; rank j adds columns j * kSlice..
+                cluster_sync();
+                const uint32_t at = static_cast<uint32_t>((quarter * 32 + lane) * L::kPitch * 4);
+                if (live) {
+#pragma unroll
+                    for (int j = 0; j < SPLIT; ++j) {
+                        const uint32_t dst = map_to_rank(a_ring, j) + rank * (kRows * L::kPitch * 4) + at;
+#pragma unroll
+                        for (int i = 0; i < L::kSlice; i += 4)
+                            st_cluster(dst + 4 * i, acc[j * L::kSlice + i], acc[j * L::kSlice + i + 1],
+                                       acc[j * L::kSlice + i + 2], acc[j * L::kSlice + i + 3]);
+                    }
+                }
+                cluster_sync();
+                if (live && ok) {
+                    float4 sum[L::kSlice / 4];
+#pragma unroll
+                    for (int r = 0; r < SPLIT; ++r) {
+                        const float4* part =
+                            reinterpret_cast<const float4*>(smem + L::kRingOff + r * (kRows * L::kPitch * 4) + at);
+#pragma unroll
+                        for (int i = 0; i < L::kSlice / 4; ++i) {
+                            const float4 q = part[i];
+                            if (r == 0) {
+                                sum[i] = q;
+                            } else {
+                                sum[i].x = __fadd_rn(sum[i].x, q.x);
+                                sum[i].y = __fadd_rn(sum[i].y, q.y);
+                                sum[i].z = __fadd_rn(sum[i].z, q.z);
+                                sum[i].w = __fadd_rn(sum[i].w, q.w);
+                            }
+                        }
+                    }
+                    store_out<L::kSlice>(p, row, col + rank * L::kSlice, [&](int i) {
+                        const float4 q = sum[i / 4];
+                        return i % 4 == 0 ? q.x : i % 4 == 1 ? q.y : i % 4 == 2 ? q.z : q.w;
+                    });
+                }
+                break;  // a cluster has one tile
             }
             if (!ok) break;
+            if (PAIR && p.tma_out) {
+                store_tma<C>(p, out_buf, lane, row - lane, col, [&](int i) { return acc[i]; });
+                continue;
+            }
             if (live)
-                store_out<C>(p, row, col, [&](int i) { return i & 1 ? hi_of(acc[i / 2]) : lo_of(acc[i / 2]); });
+                store_out<C>(p, row, col, [&](int i) { return acc[i]; });
         }
+        if (PAIR && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 2)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::kTmemCols)
-                     : "memory");
+    // PAIR: neither CTA frees its memory while the other's MMAs, commits and
+    // arrivals reach it
+    if constexpr (PAIR) cluster_sync();
+    if (warp == 2) {
+        if constexpr (PAIR)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::kTmemCols)
+                         : "memory");
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::kTmemCols)
+                         : "memory");
+    }
 }
 
 // k == 0: an empty sum
@@ -403,37 +819,114 @@ __global__ void __launch_bounds__(256) zero_kernel(T* y, int64_t m, int64_t n, i
 }
 
 // --------------------------------------------------------------- host side
-static bool encode(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, const uint8_t* p, int64_t rows,
-                   int64_t k, int64_t ld, int box_rows) {
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
-    const cuuint32_t box[2] = {kBlock, static_cast<cuuint32_t>(box_rows)};
+static bool encode(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, CUtensorMapDataType type, int bytes,
+                   const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld * bytes)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / bytes), static_cast<cuuint32_t>(box_rows)};
     const cuuint32_t es[2] = {1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return enc(map, type, 2, const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NT, bool BROW, int SPLIT>
-static cudaError_t launch(const Params& p, cudaStream_t s) {
-    using L = Layout<NT, SPLIT>;
+static int bytes_of(int dtype) { return dtype == PQ_FP32 ? 4 : 2; }
+
+// Tile width and K split of a problem: the fewest estimated microseconds among
+// the kernels, each at waves * (K blocks of a CTA * time of one + fixed). The
+// times are measured at full load (pairs: 8192 x 14336 x 4096 in 480 us;
+// 128 wide: the same in 658 us; 64 wide, two CTAs an SM: 77 x 14336 x 4096 in
+// 19 us), where row scales of B cost about twice a pair's time; the exchange
+// of a split tile about 1 us for two CTAs and half as much for each doubling
+// (1 x 4096 x 4096 without / by 2 / by 4 / by 8: 14.3 / 11.6 / 10.0 / 14 us,
+// the last with more CTAs than the SMs hold).
+struct Plan {
+    int nt, split;
+    bool pair;
+};
+static Plan plan(int64_t m, int64_t n, int64_t kb, bool brow) {
+    const int64_t sms = pq::sm_count();
+    Plan best = {128, 1, false};
+    double best_us = 1e30;
+    auto consider = [&](Plan pl, int64_t tiles, int64_t slots, double us_kb, double fixed) {
+        const int64_t waves = (tiles * pl.split + slots - 1) / slots;
+        const double us = waves * ((kb + pl.split - 1) / pl.split * us_kb + fixed);
+        if (us < best_us) {
+            best_us = us;
+            best = pl;
+        }
+    };
+    consider({256, 1, true}, (m + 255) / 256 * ((n + 255) / 256), sms / 2, brow ? 1.2 : 0.6, 6.0);
+    for (int split = 1; split <= 8 && split <= kb; split *= 2) {
+        const int64_t tm = (m + kRows - 1) / kRows;
+        const double exchange = split == 1 ? 0.0 : split == 2 ? 1.0 : split == 4 ? 1.5 : 2.0;
+        consider({128, split, false}, tm * ((n + 127) / 128), sms, brow ? 0.8 : 0.42, 5.0 + exchange);
+        consider({64, split, false}, tm * ((n + 63) / 64), 2 * sms, brow ? 0.8 : 0.42, 5.0 + exchange);
+    }
+    return best;
+}
+
+// A set-up launch: the box of A, the stages that fit beside it, the maps.
+template <int NT, bool BROW, int SPLIT, bool PAIR>
+static pq_status_t launch(Params& p, const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, int64_t k,
+                          cudaStream_t s) {
+    using L = Layout<NT, BROW, SPLIT, PAIR>;
     static bool attr_set[64] = {false};
-    auto kernel = fp8_gemm_kernel<NT, BROW, SPLIT>;
+    auto kernel = fp8_gemm_kernel<NT, BROW, SPLIT, PAIR>;
+    const int64_t tile_rows = PAIR ? 2 * kRows : kRows;
+    const int64_t tiles_m = (p.m + tile_rows - 1) / tile_rows, tiles_n = (p.n + NT - 1) / NT;
+    if (tiles_m * tiles_n > (int64_t{1} << 27)) return PQ_ERR_UNSUPPORTED;
+    p.tiles_m = static_cast<int32_t>(tiles_m);
+    p.tiles_n = static_cast<int32_t>(tiles_n);
+    // a short A brings only the rows it has: the other lanes are not read
+    const int a_rows = p.m < kRows ? static_cast<int>((p.m + 7) / 8 * 8) : kRows;
+    p.a_bytes = a_rows * kBlock;
+    p.stages = L::stages(p.a_bytes);
+    PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+    constexpr CUtensorMapDataType kByte = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    if (!enc || !encode(enc, &p.ta, kByte, 1, a, p.m, k, lda, a_rows) ||
+        !encode(enc, &p.tb, kByte, 1, b, p.n, k, ldb, L::kBRows))
+        return PQ_ERR_CUDA;
+    // TMA stores want 16-byte aligned rows
+    const int size = bytes_of(p.dtype);
+    p.tma_out = PAIR && pq::aligned(p.y, 16) && p.ldy * size % 16 == 0;
+    if (p.tma_out && !encode(enc, &p.ty, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
+                             size, p.y, p.m, p.n, p.ldy, 32))
+        return PQ_ERR_CUDA;
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
-        if (e != cudaSuccess) return e;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   L::kSmem + 1024);
+        if (e != cudaSuccess) return pq::cuda_status(e);
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
     const int tiles = p.tiles_m * p.tiles_n;
-    const int grid = SPLIT > 1 ? tiles * SPLIT : tiles < pq::sm_count() ? tiles : pq::sm_count();
-    kernel<<<grid, L::kThreads, L::kBytes, s>>>(p);
+    const int slots = L::kCtas * pq::sm_count() / L::kCluster;
+    const int grid = (SPLIT > 1 || tiles < slots ? tiles : slots) * L::kCluster;
+    kernel<<<grid, L::kThreads, L::bytes(p.a_bytes, p.stages), s>>>(p);
     pqc::count_launch();
-    return cudaGetLastError();
+    return pq::cuda_status(cudaGetLastError());
 }
 
-static int bytes_of(int dtype) { return dtype == PQ_FP32 ? 4 : 2; }
+template <bool BROW, typename... Args>
+static pq_status_t launch_plan(const Plan& pl, Args&&... args) {
+    if (pl.pair) return launch<256, BROW, 1, true>(args...);
+    if (pl.nt == 128) {
+        switch (pl.split) {
+            case 1: return launch<128, BROW, 1, false>(args...);
+            case 2: return launch<128, BROW, 2, false>(args...);
+            case 4: return launch<128, BROW, 4, false>(args...);
+            default: return launch<128, BROW, 8, false>(args...);
+        }
+    }
+    switch (pl.split) {
+        case 1: return launch<64, BROW, 1, false>(args...);
+        case 2: return launch<64, BROW, 2, false>(args...);
+        case 4: return launch<64, BROW, 4, false>(args...);
+        default: return launch<64, BROW, 8, false>(args...);
+    }
+}
 
 }  // namespace pq8
 
@@ -463,8 +956,6 @@ extern "C" pq_status_t pq_fp8_gemm(int64_t m, int64_t n, int64_t k, const uint8_
     if (n == 1) ldb = (k + 15) / 16 * 16;
     if (m > (int64_t{1} << 30) || n > (int64_t{1} << 30) || k > (int64_t{1} << 30)) return PQ_ERR_UNSUPPORTED;
     if (!pq::aligned(a, 16) || !pq::aligned(b, 16) || lda % 16 || ldb % 16) return PQ_ERR_MISALIGNED;
-    PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
-    if (!enc) return PQ_ERR_CUDA;
     Params p = {};
     p.sa = a_scale;
     p.sb = b_scale;
@@ -474,15 +965,8 @@ extern "C" pq_status_t pq_fp8_gemm(int64_t m, int64_t n, int64_t k, const uint8_
     p.ldy = ldy;
     p.kb = static_cast<int32_t>((k + kBlock - 1) / kBlock);
     p.dtype = y_dtype;
-    p.vec = pq::aligned(y, 16) && ldy * bytes_of(y_dtype) % 16 == 0;
-    constexpr int NT = 128;
-    const int64_t tiles_m = (m + kRows - 1) / kRows, tiles_n = (n + NT - 1) / NT;
-    if (tiles_m * tiles_n > (int64_t{1} << 27)) return PQ_ERR_UNSUPPORTED;
-    p.tiles_m = static_cast<int32_t>(tiles_m);
-    p.tiles_n = static_cast<int32_t>(tiles_n);
-    // a short A fills only the lanes it has: the others' sums are not read
-    const int a_rows = m < kRows ? static_cast<int>((m + 7) / 8 * 8) : kRows;
-    p.a_bytes = a_rows * kBlock;
-    if (!encode(enc, &p.ta, a, m, k, lda, a_rows) || !encode(enc, &p.tb, b, n, k, ldb, NT)) return PQ_ERR_CUDA;
-    return pq::cuda_status(b_block == PQ_BLOCK_ROW ? launch<NT, true, 1>(p, s) : launch<NT, false, 1>(p, s));
+    p.wide = pq::aligned(y, 32) && ldy * bytes_of(y_dtype) % 32 == 0;
+    const Plan pl = plan(m, n, p.kb, b_block == PQ_BLOCK_ROW);
+    return b_block == PQ_BLOCK_ROW ? launch_plan<true>(pl, p, a, lda, b, ldb, k, s)
+                                   : launch_plan<false>(pl, p, a, lda, b, ldb, k, s);
 }
