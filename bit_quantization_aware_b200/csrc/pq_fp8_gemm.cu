@@ -61,7 +61,7 @@ struct Params {
     int32_t a_bytes;     // of one A box
     int32_t stages;
     int32_t dtype;       // of y
-    int32_t wide;        // 32-byte stores of rows are aligned
+    int32_t quad;        // four elements at a multiple of four columns are aligned
     int32_t tma_out;     // y suits TMA stores
 };
 
@@ -70,22 +70,22 @@ struct Params {
 template <int NT, bool BROW, int SPLIT, bool PAIR>
 struct Layout {
     static constexpr int kCluster = PAIR ? 2 : SPLIT;
-    static constexpr int kHalves = PAIR ? 2 : 1;          // parts of the columns with their own issuer
-    static constexpr int kCols = NT / kHalves;            // columns of such a part, and of a promote thread
+    static constexpr int kParts = PAIR ? 2 : 1;           // of the columns, each with its own issuer
+    static constexpr int kCols = NT / kParts;             // columns of an MMA, and of a promote thread
     static constexpr int kBufs = PAIR ? 2 : 4;            // TMEM buffers of each part
-    static constexpr int kPromoteWarps = 4 * kHalves;
+    static constexpr int kPromoteWarps = 4 * kParts;
     static constexpr int kThreads = 128 + 32 * kPromoteWarps;
     static constexpr int kBRows = kCols / (PAIR ? 2 : 1);  // B rows of a part in a CTA
-    static constexpr int kBBytes = kHalves * kBRows * kBlock;
+    static constexpr int kBBytes = kParts * kBRows * kBlock;
     static constexpr uint32_t kTmemCols = kBufs * NT;
     static constexpr int kCtas = NT == 64 ? 2 : 1;        // resident on an SM
     // full, empty, pair [stages]; dfull, dempty [halves x buffers]; sfull,
     // sempty [scale slots]; drain [halves]; TMEM base, abort
-    static constexpr int kNumBars = 3 * kMaxStages + 2 * kHalves * kBufs + 2 * kScaleSlots + 2;
+    static constexpr int kNumBars = 3 * kMaxStages + 2 * kParts * kBufs + 2 * kScaleSlots + 2;
     static constexpr int kMiscOff = 8 * kNumBars;
     static constexpr int kScaleOff = 1024;
-    static constexpr int kOutOff = kScaleOff + (BROW ? kScaleSlots * NT * 4 : 0);  // PAIR: 4 KB a promote warp
-    static constexpr int kRingOff = kOutOff + (PAIR ? kPromoteWarps * 4096 : 0);
+    static constexpr int kOutOff = kScaleOff + (BROW ? kScaleSlots * NT * 4 : 0);  // 4 KB a promote warp
+    static constexpr int kRingOff = kOutOff + (SPLIT == 1 ? kPromoteWarps * 4096 : 0);
     static_assert(kMiscOff + 8 <= kScaleOff && kOutOff % 1024 == 0, "shared memory layout");
     // exchange of a split tile: [from rank][row][column of the slice, padded]
     static constexpr int kSlice = NT / SPLIT, kPitch = kSlice + 4;
@@ -194,16 +194,27 @@ __device__ __forceinline__ bool mbar_try_warp(uint32_t mbar, uint32_t parity) {
     return __any_sync(0xFFFFFFFFu, done);
 }
 
-// The same asked ahead: the answer to a try takes some 100 cycles and more.
+// The same asked ahead: the answer takes some 100 to 200 cycles, in which the
+// warp does other work.
+template <bool REMOTE>
 __device__ __forceinline__ uint32_t mbar_test(uint32_t mbar, uint32_t parity) {
     uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(done)
-        : "r"(mbar), "r"(parity)
-        : "memory");
+    if constexpr (REMOTE)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(done)
+            : "r"(mbar), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(done)
+            : "r"(mbar), "r"(parity)
+            : "memory");
     return done;
 }
 
@@ -280,12 +291,39 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
                  : "memory");
 }
 
+// acc += s * (v * b) on pairs of neighbours, b left out where it is 1. Two
+// values an instruction: the promote warps' arithmetic fills the issue slots
+// that the issuers' instructions wait for (8192 x 14336 x 4096: 476 us with
+// one value an instruction, 446 with two; row scales, 4096 x 4096 x 8190: 330
+// and 255), although alone, behind TMEM reads, one at a time is faster.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+    return v;
+}
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    return pair(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ void fma2(float& x, float& y, uint64_t v, uint64_t s) {
+    uint64_t a = pair(x, y);
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(v), "l"(s));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a));
+}
+
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 __device__ __forceinline__ void st_cluster(uint32_t a, float x, float y, float z, float w) {
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(x), "f"(y), "f"(z), "f"(w)
                  : "memory");
+}
+__device__ __forceinline__ void st_cluster(uint32_t a, float x, float y) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(x), "f"(y) : "memory");
 }
 __device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
     uint32_t a;
@@ -312,88 +350,115 @@ __device__ __forceinline__ void tile_of(const Params& p, int t, int& tm, int& tn
     tn = r / rows;
 }
 
-// Rounds v(0..N) and writes it to N columns of a row of which `left` exist.
-// WIDE: 32-byte stores, whole sectors of a thread's own row.
-template <typename T, int N, typename F>
-__device__ __forceinline__ void store_row(T* y, int64_t left, bool wide, F&& v) {
-    constexpr int W = 32 / sizeof(T) < N ? 32 / sizeof(T) : N;  // elements of a store
+// Where a promote thread's C sums are. ROWS false: row `lane` of its warp's
+// 32, columns 0..C-1. ROWS true: rows lane / 4 + 8 i for i < 4, columns
+// 8 j + 2 (lane % 4) + e for e < 2, at acc[8 j + 2 i + e] (tmem_ld_rows).
+
+// A warp's 32 rows x C columns to y by way of its 4 KB of shared memory, 128
+// bytes of each row at a time (the 128B swizzle: 16-byte chunk c of row r at
+// chunk c ^ (r % 8), so the writes are free of bank conflicts), and from there
+// by the TMA engine, which clips what lies beyond y, or, where y does not suit
+// it, row by row. Direct stores of whole sectors of each thread's row took
+// 5000 cycles a tile, during which no K block left TMEM; element by element
+// (an odd pitch) they made up most of a small product's time.
+template <typename T, int C, bool ROWS>
+__device__ __forceinline__ void store_typed(const Params& p, uint32_t buf, int lane, int64_t row0, int64_t col,
+                                            const float (&acc)[C]) {
+    constexpr int W = 128 / sizeof(T);  // columns of a round
+    constexpr int B = sizeof(T);
 #pragma unroll
-    for (int c = 0; c < N; c += W) {
+    for (int c = 0; c < C; c += W) {
+        if (p.tma_out && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
         union {
-            T e[W];
-            uint32_t w[W * sizeof(T) / 4];
+            T e[16 / B];
+            uint32_t w[4];
         } o;
+        if constexpr (ROWS) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) o.e[i] = static_cast<T>(v(c + i));
-        if (wide && c + W <= left) {
-            if constexpr (W * sizeof(T) == 32)
-                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(y + c), "r"(o.w[0]),
-                             "r"(o.w[1]), "r"(o.w[2]), "r"(o.w[3]), "r"(o.w[4]), "r"(o.w[5]), "r"(o.w[6]),
-                             "r"(o.w[7])
-                             : "memory");
-            else
-                *reinterpret_cast<uint4*>(y + c) = make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
+            for (int j = 0; j < W / 8; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = lane / 4 + 8 * i, at = (8 * j + 2 * (lane % 4)) * B;
+                    const uint32_t dst = buf + row * 128 + (((at >> 4) ^ (row & 7)) << 4) + (at & 15);
+                    o.e[0] = static_cast<T>(acc[c + 8 * j + 2 * i]);
+                    o.e[1] = static_cast<T>(acc[c + 8 * j + 2 * i + 1]);
+                    if constexpr (B == 4)
+                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(o.w[0]), "r"(o.w[1]) : "memory");
+                    else
+                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(o.w[0]) : "memory");
+                }
         } else {
 #pragma unroll
-            for (int i = 0; i < W; ++i)
-                if (c + i < left) y[c + i] = o.e[i];
+            for (int q = 0; q < 8; ++q) {
+#pragma unroll
+                for (int i = 0; i < 16 / B; ++i) o.e[i] = static_cast<T>(acc[c + q * (16 / B) + i]);
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 buf + lane * 128 + ((q ^ (lane & 7)) << 4)),
+                             "r"(o.w[0]), "r"(o.w[1]), "r"(o.w[2]), "r"(o.w[3])
+                             : "memory");
+            }
+        }
+        if (p.tma_out) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0 && row0 < p.m && col + c < p.n) {
+                asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                                 reinterpret_cast<uint64_t>(&p.ty)),
+                             "r"(buf), "r"(static_cast<int32_t>(col + c)), "r"(static_cast<int32_t>(row0))
+                             : "memory");
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+            continue;
+        }
+        __syncwarp();
+        const int rows = p.m - row0 < 32 ? static_cast<int>(p.m - row0) : 32;  // <= 0: none
+        const int at = c + lane * (4 / B);  // this lane's column: 4 bytes of each row
+        const int left = p.n - col - at < 2 ? static_cast<int>(p.n - col - at) : 2;
+        T* y = static_cast<T*>(p.y) + row0 * p.ldy + col + at;
+        for (int r = 0; r < rows; ++r, y += p.ldy) {
+            asm volatile("ld.shared.b32 %0, [%1];"
+                         : "=r"(o.w[0])
+                         : "r"(buf + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + ((lane & 3) << 2)));
+            if constexpr (B == 4) {
+                if (left > 0) *y = o.e[0];
+            } else if (left == 2 && (reinterpret_cast<uintptr_t>(y) & 3) == 0) {
+                *reinterpret_cast<uint32_t*>(y) = o.w[0];
+            } else {
+                if (left > 0) y[0] = o.e[0];
+                if (left > 1) y[1] = o.e[1];
+            }
         }
     }
 }
 
-template <int N, typename F>
-__device__ __forceinline__ void store_out(const Params& p, int64_t row, int64_t col, F&& v) {
-    const int64_t left = p.n - col;
-    const int64_t at = row * p.ldy + col;
-    if (p.dtype == PQ_BF16) store_row<__nv_bfloat16, N>(static_cast<__nv_bfloat16*>(p.y) + at, left, p.wide, v);
-    else if (p.dtype == PQ_FP16) store_row<__half, N>(static_cast<__half*>(p.y) + at, left, p.wide, v);
-    else store_row<float, N>(static_cast<float*>(p.y) + at, left, p.wide, v);
+template <int C, bool ROWS>
+__device__ __forceinline__ void store(const Params& p, uint32_t buf, int lane, int64_t row0, int64_t col,
+                                      const float (&acc)[C]) {
+    if (p.dtype == PQ_BF16) store_typed<__nv_bfloat16, C, ROWS>(p, buf, lane, row0, col, acc);
+    else if (p.dtype == PQ_FP16) store_typed<__half, C, ROWS>(p, buf, lane, row0, col, acc);
+    else store_typed<float, C, ROWS>(p, buf, lane, row0, col, acc);
 }
 
-// A warp's 32 rows x N columns through its 4 KB of shared memory and the TMA
-// engine, 128 bytes of each row at a time (the 128B swizzle: 16-byte chunk c
-// of row r at chunk c ^ (r % 8), so the writes are free of bank conflicts).
-// Rows and columns beyond y are clipped. Direct stores of whole sectors a
-// thread took 5000 cycles a tile, during which no K block left TMEM.
-template <typename T, int N, typename F>
-__device__ __forceinline__ void store_tma_typed(const Params& p, uint32_t buf, int lane, int64_t row0, int64_t col,
-                                                F&& v) {
-    constexpr int W = 128 / sizeof(T);  // columns of a round
+// Four consecutive elements of a row of which `left` exist.
+template <typename T>
+__device__ __forceinline__ void store4(T* y, int64_t left, bool whole, const float4& v) {
+    union {
+        T e[4];
+        uint32_t w[sizeof(T)];
+    } o;
+    o.e[0] = static_cast<T>(v.x);
+    o.e[1] = static_cast<T>(v.y);
+    o.e[2] = static_cast<T>(v.z);
+    o.e[3] = static_cast<T>(v.w);
+    if (whole && left >= 4) {
+        if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(y) = make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
+        else *reinterpret_cast<uint2*>(y) = make_uint2(o.w[0], o.w[1]);
+    } else {
 #pragma unroll
-    for (int c = 0; c < N; c += W) {
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        __syncwarp();
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            union {
-                T e[16 / sizeof(T)];
-                uint32_t w[4];
-            } o;
-#pragma unroll
-            for (int i = 0; i < 16 / static_cast<int>(sizeof(T)); ++i)
-                o.e[i] = static_cast<T>(v(c + q * (16 / static_cast<int>(sizeof(T))) + i));
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             buf + lane * 128 + ((q ^ (lane & 7)) << 4)),
-                         "r"(o.w[0]), "r"(o.w[1]), "r"(o.w[2]), "r"(o.w[3])
-                         : "memory");
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0 && row0 < p.m && col + c < p.n) {
-            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                             reinterpret_cast<uint64_t>(&p.ty)),
-                         "r"(buf), "r"(static_cast<int32_t>(col + c)), "r"(static_cast<int32_t>(row0))
-                         : "memory");
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        }
+        for (int i = 0; i < 4; ++i)
+            if (i < left) y[i] = o.e[i];
     }
-}
-
-template <int N, typename F>
-__device__ __forceinline__ void store_tma(const Params& p, uint32_t buf, int lane, int64_t row0, int64_t col, F&& v) {
-    if (p.dtype == PQ_BF16) store_tma_typed<__nv_bfloat16, N>(p, buf, lane, row0, col, v);
-    else if (p.dtype == PQ_FP16) store_tma_typed<__half, N>(p, buf, lane, row0, col, v);
-    else store_tma_typed<float, N>(p, buf, lane, row0, col, v);
 }
 
 template <int NT, bool BROW, int SPLIT, bool PAIR>
@@ -406,7 +471,7 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
                                                ~uintptr_t{1023});
     const uint32_t sbase = smem_u32(smem);
     const uint32_t b_full = sbase, b_empty = b_full + 8u * kMaxStages, b_pair = b_empty + 8u * kMaxStages;
-    constexpr uint32_t kD = 8u * L::kHalves * L::kBufs;
+    constexpr uint32_t kD = 8u * L::kParts * L::kBufs;
     const uint32_t b_dfull = b_pair + 8u * kMaxStages, b_dempty = b_dfull + kD;
     const uint32_t b_sfull = b_dempty + kD, b_sempty = b_sfull + 8u * kScaleSlots;
     const uint32_t b_drain = b_sempty + 8u * kScaleSlots;
@@ -419,18 +484,18 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
     if (tid == 0) {
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(b_full + 8u * s, 1);
-            mbar_init(b_empty + 8u * s, L::kHalves);
+            mbar_init(b_empty + 8u * s, L::kParts);
             mbar_init(b_pair + 8u * s, 1);
         }
-        for (int b = 0; b < L::kHalves * L::kBufs; ++b) {
+        for (int b = 0; b < L::kParts * L::kBufs; ++b) {
             mbar_init(b_dfull + 8u * b, 1);
-            mbar_init(b_dempty + 8u * b, PAIR ? 8 : 4);  // a half's promote warps, of both CTAs
+            mbar_init(b_dempty + 8u * b, PAIR ? 8 : 4);  // the part's promote warps, of both CTAs
         }
         for (int s = 0; s < kScaleSlots; ++s) {
             mbar_init(b_sfull + 8u * s, 32);
             mbar_init(b_sempty + 8u * s, L::kPromoteWarps);
         }
-        for (int h = 0; h < L::kHalves; ++h) mbar_init(b_drain + 8u * h, 1);
+        for (int h = 0; h < L::kParts; ++h) mbar_init(b_drain + 8u * h, 1);
         const int forced = *static_cast<volatile int*>(&g_force_abort);
         *abort = forced;
         if (forced) atomicExch(&g_status, 1);
@@ -456,6 +521,10 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
     if constexpr (PAIR) cluster_sync();  // the other CTA's barriers are there
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // the launch before this one in the stream may still run (its results are
+    // read from here on), and the next one may begin its own set-up
+    cudaGridDependencySynchronize();
+    cudaTriggerProgrammaticLaunchCompletion();
 
     // this CTA's tiles, its K blocks of each, its rows within a tile
     const int tiles = p.tiles_m * p.tiles_n;
@@ -492,7 +561,7 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
                         mbar_expect_tx(bar, static_cast<uint32_t>(p.a_bytes) + L::kBBytes);
                         tma_load_2d(a_ring + r.idx * p.a_bytes, &p.ta, bar, kb * kBlock, ra);
 #pragma unroll
-                        for (int h = 0; h < L::kHalves; ++h)
+                        for (int h = 0; h < L::kParts; ++h)
                             tma_load_2d(b_ring + r.idx * L::kBBytes + h * L::kBRows * kBlock, &p.tb, bar, kb * kBlock,
                                         rb + h * L::kCols);
                         r.next();
@@ -510,7 +579,7 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
                 }
             }
             __syncwarp();
-        } else if (warp == 1 || (PAIR && warp == 3 && rank == 0)) {
+        } else if (warp == 1 || (L::kParts == 2 && warp == 3 && rank == 0)) {
             if (!PAIR || rank == 0) {
                 // ------------------------------------------------ MMA issuer
                 // The whole warp walks the loop and one lane issues: the
@@ -523,20 +592,33 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
                 StageRing r(p.stages);
                 Ring<L::kBufs> d;
                 bool ok = true;
+                // Three waits one after the other took most of a K block's
+                // time, so the next block's are asked for before this one's
+                // MMAs (512 x 4096 x 4096: 15.9 -> 15.2 us). A pair's two
+                // issuers have the time: asking ahead cost them 2%.
+                constexpr bool kAhead = L::kParts == 1;
+                uint32_t ready = 0;
                 for (int t = first; ok && t < tiles; t += step) {
                     for (int kb = k0; kb < k1; ++kb) {
                         const uint64_t a = sw128_desc(a_ring + r.idx * p.a_bytes);
                         const uint64_t b = sw128_desc(b_ring + r.idx * L::kBBytes + h * L::kBRows * kBlock);
-                        const uint32_t acc = tmem + (d.idx * L::kHalves + h) * L::kCols;
+                        const uint32_t acc = tmem + (d.idx * L::kParts + h) * L::kCols;
                         const uint32_t free_bar = b_empty + 8u * r.idx, full_bar = dfull + 8u * d.idx;
-                        // operands first: they are early, the buffer is what the loop waits for
-                        if (!uniform_wait<false>(b_full + 8u * r.idx, r.phase, abort) ||
-                            (PAIR && !uniform_wait<true>(b_pair + 8u * r.idx, r.phase, abort)) ||
-                            !uniform_wait<PAIR>(dempty + 8u * d.idx, d.phase ^ 1u, abort)) {
+                        if (!(kAhead && __any_sync(0xFFFFFFFFu, ready)) &&
+                            (!uniform_wait<false>(b_full + 8u * r.idx, r.phase, abort) ||
+                             (PAIR && !uniform_wait<true>(b_pair + 8u * r.idx, r.phase, abort)) ||
+                             !uniform_wait<PAIR>(dempty + 8u * d.idx, d.phase ^ 1u, abort))) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
+                        r.next();
+                        d.next();
+                        if constexpr (kAhead) {
+                            ready = mbar_test<false>(b_full + 8u * r.idx, r.phase) &
+                                    mbar_test<PAIR>(dempty + 8u * d.idx, d.phase ^ 1u);
+                            if constexpr (PAIR) ready &= mbar_test<true>(b_pair + 8u * r.idx, r.phase);
+                        }
                         if (one) {
 #pragma unroll
                             for (int k = 0; k < kBlock / 32; ++k)
@@ -545,8 +627,6 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
                             commit<PAIR>(free_bar);
                         }
                         __syncwarp();
-                        r.next();
-                        d.next();
                     }
                 }
                 // every MMA completes before TMEM is freed
@@ -570,7 +650,7 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
                         r.next();
                     }
                 if (one)  // the issuers' last arrivals here
-                    for (int h = 0; h < L::kHalves; ++h) mbar_drain(b_drain + 8u * h, 0);
+                    for (int h = 0; h < L::kParts; ++h) mbar_drain(b_drain + 8u * h, 0);
             }
             __syncwarp();
         } else if (warp == 2) {
@@ -606,11 +686,11 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
     } else {
         if constexpr (kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         // ------------------------------------------------------- promote
-        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        const int quarter = warp & 3, part = (warp - 4) >> 2;
         const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
         constexpr int C = L::kCols;
-        const uint32_t dfull = b_dfull + 8u * L::kBufs * half;
-        const uint32_t dempty0 = b_dempty + 8u * L::kBufs * half;
+        const uint32_t dfull = b_dfull + 8u * L::kBufs * part;
+        const uint32_t dempty0 = b_dempty + 8u * L::kBufs * part;
         const uint32_t dempty = PAIR ? map_to_rank(dempty0, 0) : dempty0;  // the issuer's
         const uint32_t out_buf = sbase + L::kOutOff + (warp - 4) * 4096;
         Ring<L::kBufs> d;
@@ -623,12 +703,11 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
             if constexpr (PAIR) mbar_arrive_cluster_if(bar, one);
             else mbar_arrive_if(bar, one);
         };
-        auto buffer = [&]() { return tmem + lane_addr + (d.idx * L::kHalves + half) * C; };
+        auto buffer = [&]() { return tmem + lane_addr + d.idx * NT + part * C; };
         // The tile's K blocks into acc, tile scales: an element is one
         // multiply-add behind a TMEM read. The reads run one chunk ahead of
         // the arithmetic, across K blocks too; whether the next block is
-        // there is asked two chunks before. (Paired multiply-adds, f32x2,
-        // measured slower: 54 against 42 cycles a warp and 32 columns.)
+        // there is asked two chunks before.
         auto sum_blocks_tile = [&](float(&acc)[C], int64_t row, int64_t col) -> bool {
             constexpr int W = NT == 64 ? 16 : 32;  // columns of a read (registers)
             // rows, columns and K blocks beyond the last take the last one's
@@ -665,14 +744,14 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
                 uint32_t ready = 0;
                 auto add = [&](int c) {
 #pragma unroll
-                    for (int i = 0; i < W; ++i)
-                        acc[c + i] = __fmaf_rn(__uint_as_float(v[c / W % 2][i]), s, acc[c + i]);
+                    for (int i = 0; i < W; i += 2)
+                        fma2(acc[c + i], acc[c + i + 1], pair(v[c / W % 2][i], v[c / W % 2][i + 1]), pair(s, s));
                 };
 #pragma unroll
                 for (int c = 0; c + W < C; c += W) {
                     tmem_wait(v[c / W % 2]);
                     tmem_ld(src + c + W, v[(c / W + 1) % 2]);
-                    if (c + 3 * W == C) ready = mbar_test(dfull + 8u * d.idx, d.phase);
+                    if (c == (C > 3 * W ? C - 3 * W : 0)) ready = mbar_test<false>(dfull + 8u * d.idx, d.phase);
                     add(c);
                 }
                 tmem_wait(v[(C / W - 1) % 2]);
@@ -695,105 +774,137 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
             return true;
         };
         // The same with row scales of B, in shared memory: an element is a
-        // multiplication and a multiply-add.
-        auto sum_blocks_row = [&](float(&acc)[C], int64_t row, int64_t col) -> bool {
-            const bool live = row < p.m;
-            const float* sa = p.sa + (live ? row : 0);
-            float next = live && k0 < k1 ? __ldg(sa + k0 * p.m) : 0.0f;
-            for (int kb = k0; kb < k1; ++kb) {
-                const float s = next;
-                next = live && kb + 1 < k1 ? __ldg(sa + (kb + 1) * p.m) : 0.0f;
+        // multiplication and a multiply-add. With a whole row on a thread,
+        // every scale of the K block would pass through every thread (1024
+        // cycles of shared memory a block); read 16 lanes x 8 columns at a
+        // time, a thread has a quarter of the columns and four rows.
+        auto sum_blocks_row = [&](float(&acc)[C], int64_t row0, int64_t) -> bool {
+            const float* sa[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t row = row0 + lane / 4 + 8 * i;
+                sa[i] = p.sa + (row < p.m ? row : p.m - 1);
+            }
+            float a0[4], a1[4], a[4];  // A's scales of the next two K blocks, and of this one
+            auto fetch = [&](int kb, float(&to)[4]) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) to[i] = __ldg(sa[i] + min(kb, k1 - 1) * p.m);
+            };
+            if (k0 >= k1) return true;
+            fetch(k0, a0);
+            fetch(k0 + 1, a1);
+            auto block = [&](int kb, float(&next)[4]) -> bool {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i] = next[i];
+                fetch(kb + 2, next);
                 if (!uniform_wait<false>(b_sfull + 8u * sr.idx, sr.phase, abort) ||
                     !uniform_wait<false>(dfull + 8u * d.idx, d.phase, abort))
                     return false;
                 tc_fence_after();
-                const float4* bs = reinterpret_cast<const float4*>(scales + sr.idx * NT + half * C);
+                const float* bs = scales + sr.idx * NT + part * C + 2 * (lane % 4);
+                const uint32_t src = buffer();
+                uint32_t v[2][16];  // 32 columns of 16 rows: reads run one ahead
+                tmem_ld_rows(src, v[0]);
 #pragma unroll
                 for (int c = 0; c < C; c += 32) {
-                    uint32_t v[32];
-                    tmem_ld(buffer() + c, v);
-                    tmem_wait(v);
-                    if (c + 32 == C) free_buffer(dempty + 8u * d.idx);
+                    float2 b[4];
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 b = bs[(c + i) / 4];
-                        acc[c + i] = __fmaf_rn(__fmul_rn(__uint_as_float(v[i]), b.x), s, acc[c + i]);
-                        acc[c + i + 1] = __fmaf_rn(__fmul_rn(__uint_as_float(v[i + 1]), b.y), s, acc[c + i + 1]);
-                        acc[c + i + 2] = __fmaf_rn(__fmul_rn(__uint_as_float(v[i + 2]), b.z), s, acc[c + i + 2]);
-                        acc[c + i + 3] = __fmaf_rn(__fmul_rn(__uint_as_float(v[i + 3]), b.w), s, acc[c + i + 3]);
+                    for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float2*>(bs + c + 8 * j);
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        tmem_wait(v[g]);
+                        if (g == 0) tmem_ld_rows(src + c + (16u << 16), v[1]);
+                        else if (c + 32 < C) tmem_ld_rows(src + c + 32, v[0]);
+                        else free_buffer(dempty + 8u * d.idx);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int o = c + 8 * j + 2 * (2 * g + h);
+                                fma2(acc[o], acc[o + 1],
+                                     mul2(pair(v[g][4 * j + 2 * h], v[g][4 * j + 2 * h + 1]), pair(b[j].x, b[j].y)),
+                                     pair(a[2 * g + h], a[2 * g + h]));
+                            }
                     }
                 }
                 __syncwarp();
                 mbar_arrive_if(b_sempty + 8u * sr.idx, one);
                 sr.next();
                 d.next();
+                return true;
+            };
+            for (int kb = k0; kb < k1; kb += 2) {
+                if (!block(kb, a0)) return false;
+                if (kb + 1 < k1 && !block(kb + 1, a1)) return false;
             }
             return true;
         };
         auto sum_blocks = [&](float(&acc)[C], int64_t row, int64_t col) -> bool {
             if constexpr (BROW) return sum_blocks_row(acc, row, col);
-            else return sum_blocks_tile(acc, row, col);
+            else return sum_blocks_tile(acc, row + lane, col);
         };
         for (int t = first; ok && t < tiles; t += step) {
             int tm, tn;
             tile_of(p, t, tm, tn);
-            const int64_t row = static_cast<int64_t>(tm) * kTileRows + row_off + quarter * 32 + lane;
-            const int64_t col = static_cast<int64_t>(tn) * NT + half * C;
-            const bool live = row < p.m;
+            const int64_t row0 = static_cast<int64_t>(tm) * kTileRows + row_off + quarter * 32;  // the warp's
+            const int64_t col = static_cast<int64_t>(tn) * NT + part * C;
             float acc[C];
 #pragma unroll
             for (int i = 0; i < C; ++i) acc[i] = 0.0f;
-            ok = sum_blocks(acc, row, col);
+            ok = sum_blocks(acc, row0, col);
             if constexpr (SPLIT > 1) {
-                // every CTA's stages are free; rank j adds columns j * kSlice..
-                cluster_sync();
-                const uint32_t at = static_cast<uint32_t>((quarter * 32 + lane) * L::kPitch * 4);
-                if (live) {
+                constexpr int kPart = kRows * L::kPitch * 4;  // bytes of a rank's sums of a slice
+                cluster_sync();  // every CTA's stages are free; rank j adds columns j * kSlice..
 #pragma unroll
-                    for (int j = 0; j < SPLIT; ++j) {
-                        const uint32_t dst = map_to_rank(a_ring, j) + rank * (kRows * L::kPitch * 4) + at;
+                for (int j = 0; j < SPLIT; ++j) {
+                    const uint32_t dst = map_to_rank(a_ring, j) + rank * kPart;
+                    if constexpr (BROW) {
 #pragma unroll
-                        for (int i = 0; i < L::kSlice; i += 4)
-                            st_cluster(dst + 4 * i, acc[j * L::kSlice + i], acc[j * L::kSlice + i + 1],
-                                       acc[j * L::kSlice + i + 2], acc[j * L::kSlice + i + 3]);
+                        for (int i = 0; i < 4; ++i) {
+                            const int row = lane / 4 + 8 * i;
+                            if (row0 + row < p.m)
+#pragma unroll
+                                for (int c = 0; c < L::kSlice; c += 8)
+                                    st_cluster(dst + ((quarter * 32 + row) * L::kPitch + c + 2 * (lane % 4)) * 4,
+                                               acc[j * L::kSlice + c + 2 * i], acc[j * L::kSlice + c + 2 * i + 1]);
+                        }
+                    } else if (row0 + lane < p.m) {
+#pragma unroll
+                        for (int c = 0; c < L::kSlice; c += 4)
+                            st_cluster(dst + ((quarter * 32 + lane) * L::kPitch + c) * 4, acc[j * L::kSlice + c],
+                                       acc[j * L::kSlice + c + 1], acc[j * L::kSlice + c + 2],
+                                       acc[j * L::kSlice + c + 3]);
                     }
                 }
                 cluster_sync();
-                if (live && ok) {
-                    float4 sum[L::kSlice / 4];
+                // four columns a thread, neighbours along the row
+                constexpr int kQuads = L::kSlice / 4;
+                const int64_t tile_row = static_cast<int64_t>(tm) * kRows;
+                const int rows = p.m - tile_row < kRows ? static_cast<int>(p.m - tile_row) : kRows;
+                for (int i = tid - 128; ok && i < rows * kQuads; i += 32 * L::kPromoteWarps) {
+                    const int row = i / kQuads, c = i % kQuads * 4;
+                    const uint8_t* part = smem + L::kRingOff + (row * L::kPitch + c) * 4;
+                    float4 sum = *reinterpret_cast<const float4*>(part);
 #pragma unroll
-                    for (int r = 0; r < SPLIT; ++r) {
-                        const float4* part =
-                            reinterpret_cast<const float4*>(smem + L::kRingOff + r * (kRows * L::kPitch * 4) + at);
-#pragma unroll
-                        for (int i = 0; i < L::kSlice / 4; ++i) {
-                            const float4 q = part[i];
-                            if (r == 0) {
-                                sum[i] = q;
-                            } else {
-                                sum[i].x = __fadd_rn(sum[i].x, q.x);
-                                sum[i].y = __fadd_rn(sum[i].y, q.y);
-                                sum[i].z = __fadd_rn(sum[i].z, q.z);
-                                sum[i].w = __fadd_rn(sum[i].w, q.w);
-                            }
-                        }
+                    for (int r = 1; r < SPLIT; ++r) {
+                        const float4 q = *reinterpret_cast<const float4*>(part + r * kPart);
+                        sum.x = __fadd_rn(sum.x, q.x);
+                        sum.y = __fadd_rn(sum.y, q.y);
+                        sum.z = __fadd_rn(sum.z, q.z);
+                        sum.w = __fadd_rn(sum.w, q.w);
                     }
-                    store_out<L::kSlice>(p, row, col + rank * L::kSlice, [&](int i) {
-                        const float4 q = sum[i / 4];
-                        return i % 4 == 0 ? q.x : i % 4 == 1 ? q.y : i % 4 == 2 ? q.z : q.w;
-                    });
+                    const int64_t cc = col + rank * L::kSlice + c, at = (tile_row + row) * p.ldy + cc;
+                    if (p.dtype == PQ_BF16) store4(static_cast<__nv_bfloat16*>(p.y) + at, p.n - cc, p.quad, sum);
+                    else if (p.dtype == PQ_FP16) store4(static_cast<__half*>(p.y) + at, p.n - cc, p.quad, sum);
+                    else store4(static_cast<float*>(p.y) + at, p.n - cc, p.quad, sum);
                 }
                 break;  // a cluster has one tile
+            } else {
+                if (!ok) break;
+                store<C, BROW>(p, out_buf, lane, row0, col, acc);
             }
-            if (!ok) break;
-            if (PAIR && p.tma_out) {
-                store_tma<C>(p, out_buf, lane, row - lane, col, [&](int i) { return acc[i]; });
-                continue;
-            }
-            if (live)
-                store_out<C>(p, row, col, [&](int i) { return acc[i]; });
         }
-        if (PAIR && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 
     tc_fence_before();
@@ -832,36 +943,72 @@ static bool encode(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, CUte
 
 static int bytes_of(int dtype) { return dtype == PQ_FP32 ? 4 : 2; }
 
-// Tile width and K split of a problem: the fewest estimated microseconds among
-// the kernels, each at waves * (K blocks of a CTA * time of one + fixed). The
-// times are measured at full load (pairs: 8192 x 14336 x 4096 in 480 us;
-// 128 wide: the same in 658 us; 64 wide, two CTAs an SM: 77 x 14336 x 4096 in
-// 19 us), where row scales of B cost about twice a pair's time; the exchange
-// of a split tile about 1 us for two CTAs and half as much for each doubling
-// (1 x 4096 x 4096 without / by 2 / by 4 / by 8: 14.3 / 11.6 / 10.0 / 14 us,
-// the last with more CTAs than the SMs hold).
+// Clusters of a split kernel that the GPU holds at a time (a cluster lives in
+// one GPC, so 8 CTAs of a whole SM each fit fewer times than SMs / 8).
+template <int NT, int SPLIT>
+static int64_t clusters_resident() {
+    using L = Layout<NT, false, SPLIT, false>;
+    static int cached[64] = {0};
+    const int dev = pq::current_device();
+    if (cached[dev] == 0) {
+        auto kernel = fp8_gemm_kernel<NT, false, SPLIT, false>;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(SPLIT);
+        cfg.blockDim = dim3(L::kThreads);
+        cfg.dynamicSmemBytes = L::kSmem + 1024;
+        int n = 0;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem + 1024) !=
+                cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+            cudaGetLastError();  // the estimate stands in
+            n = L::kCtas * pq::sm_count() / (SPLIT + 1);
+        }
+        cached[dev] = n;
+    }
+    return cached[dev];
+}
+
+// Tile width and K split of a problem: the least estimated time
+//   4 + waves * (K blocks of a CTA * time of one + 1 + exchange) microseconds
+// among the kernels. The times of a K block fit what they measured, tile
+// scales / row scales: pairs 0.5 / 0.85 (8192 x 14336 x 4096: 449 us;
+// 4096 x 4096 x 8190 by rows: 209), 128 wide 0.28 / 0.6 (512 x 4096 x 4096:
+// 14.0, in pairs 19.6), 64 wide 0.24 / 0.45, or 0.36 / 0.55 where two CTAs
+// share an SM (77 x 14336 x 4096: 17.0, 128 wide 14.7). The exchange of a
+// split grows with the sums that it moves: 1 x 4096 x 4096 took 13.5 us in
+// one piece, 10.6 by 2 and 8.0 by 4; 300 x 700 x 2000 (64 wide) 9.7, 8.0 and 7.9.
 struct Plan {
     int nt, split;
     bool pair;
 };
 static Plan plan(int64_t m, int64_t n, int64_t kb, bool brow) {
     const int64_t sms = pq::sm_count();
+    const double rows = m < kRows ? static_cast<double>(m) / kRows : 1.0;
     Plan best = {128, 1, false};
     double best_us = 1e30;
-    auto consider = [&](Plan pl, int64_t tiles, int64_t slots, double us_kb, double fixed) {
-        const int64_t waves = (tiles * pl.split + slots - 1) / slots;
-        const double us = waves * ((kb + pl.split - 1) / pl.split * us_kb + fixed);
+    auto consider = [&](Plan pl, int64_t tiles, int64_t resident, double us_kb, double exchange) {
+        const int64_t waves = (tiles + resident - 1) / resident;
+        const double us = waves * ((kb + pl.split - 1) / pl.split * us_kb + 1.0 + exchange);
         if (us < best_us) {
             best_us = us;
             best = pl;
         }
     };
-    consider({256, 1, true}, (m + 255) / 256 * ((n + 255) / 256), sms / 2, brow ? 1.2 : 0.6, 6.0);
+    consider({256, 1, true}, (m + 255) / 256 * ((n + 255) / 256), sms / 2, brow ? 0.85 : 0.5, 0.0);
+    const int64_t tm = (m + kRows - 1) / kRows, t128 = tm * ((n + 127) / 128), t64 = tm * ((n + 63) / 64);
     for (int split = 1; split <= 8 && split <= kb; split *= 2) {
-        const int64_t tm = (m + kRows - 1) / kRows;
-        const double exchange = split == 1 ? 0.0 : split == 2 ? 1.0 : split == 4 ? 1.5 : 2.0;
-        consider({128, split, false}, tm * ((n + 127) / 128), sms, brow ? 0.8 : 0.42, 5.0 + exchange);
-        consider({64, split, false}, tm * ((n + 63) / 64), 2 * sms, brow ? 0.8 : 0.42, 5.0 + exchange);
+        const int64_t c128 = split == 1   ? sms
+                             : split == 2 ? clusters_resident<128, 2>()
+                             : split == 4 ? clusters_resident<128, 4>()
+                                          : clusters_resident<128, 8>();
+        const int64_t c64 = split == 1   ? 2 * sms
+                            : split == 2 ? clusters_resident<64, 2>()
+                            : split == 4 ? clusters_resident<64, 4>()
+                                         : clusters_resident<64, 8>();
+        const double moved = split == 1 ? 0.0 : 0.3 + rows * (split == 2 ? 1.2 : split == 4 ? 2.5 : 5.0);
+        consider({128, split, false}, t128, c128, brow ? 0.6 : 0.28, moved);
+        const bool shared = t64 * split > sms;
+        consider({64, split, false}, t64, c64, brow ? (shared ? 0.55 : 0.45) : (shared ? 0.36 : 0.24), moved / 2);
     }
     return best;
 }
@@ -889,7 +1036,7 @@ static pq_status_t launch(Params& p, const uint8_t* a, int64_t lda, const uint8_
         return PQ_ERR_CUDA;
     // TMA stores want 16-byte aligned rows
     const int size = bytes_of(p.dtype);
-    p.tma_out = PAIR && pq::aligned(p.y, 16) && p.ldy * size % 16 == 0;
+    p.tma_out = SPLIT == 1 && pq::aligned(p.y, 16) && p.ldy * size % 16 == 0;
     if (p.tma_out && !encode(enc, &p.ty, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
                              size, p.y, p.m, p.n, p.ldy, 32))
         return PQ_ERR_CUDA;
@@ -904,9 +1051,19 @@ static pq_status_t launch(Params& p, const uint8_t* a, int64_t lda, const uint8_
     const int tiles = p.tiles_m * p.tiles_n;
     const int slots = L::kCtas * pq::sm_count() / L::kCluster;
     const int grid = (SPLIT > 1 || tiles < slots ? tiles : slots) * L::kCluster;
-    kernel<<<grid, L::kThreads, L::bytes(p.a_bytes, p.stages), s>>>(p);
-    pqc::count_launch();
-    return pq::cuda_status(cudaGetLastError());
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(L::kThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(L::bytes(p.a_bytes, p.stages));
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+    if (e == cudaSuccess) pqc::count_launch();
+    return pq::cuda_status(e);
 }
 
 template <bool BROW, typename... Args>
@@ -965,7 +1122,7 @@ extern "C" pq_status_t pq_fp8_gemm(int64_t m, int64_t n, int64_t k, const uint8_
     p.ldy = ldy;
     p.kb = static_cast<int32_t>((k + kBlock - 1) / kBlock);
     p.dtype = y_dtype;
-    p.wide = pq::aligned(y, 32) && ldy * bytes_of(y_dtype) % 32 == 0;
+    p.quad = pq::aligned(y, 4 * bytes_of(y_dtype)) && ldy % 4 == 0;
     const Plan pl = plan(m, n, p.kb, b_block == PQ_BLOCK_ROW);
     return b_block == PQ_BLOCK_ROW ? launch_plan<true>(pl, p, a, lda, b, ldb, k, s)
                                    : launch_plan<false>(pl, p, a, lda, b, ldb, k, s);

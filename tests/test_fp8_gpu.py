@@ -126,7 +126,8 @@ def check_product(pq, m, n, k, block, out, seed=0, std=1.0):
 
 PRODUCTS = [(1, 1, 1), (1, 128, 128), (1, 4096, 4096), (2, 130, 257), (7, 64, 8192), (16, 1024, 4096),
             (77, 1000, 1536), (128, 128, 128), (129, 127, 130), (130, 256, 384), (255, 513, 1000),
-            (300, 2048, 640), (512, 512, 4111), (1000, 5632, 2048), (64, 14336, 512)]
+            (300, 2048, 640), (512, 512, 4111), (1000, 5632, 2048), (64, 14336, 512),
+            (2048, 2050, 384), (1990, 4099, 200), (2300, 2048, 100)]
 
 
 @pytest.mark.parametrize("block", [R.TILE, R.ROW])
@@ -137,7 +138,7 @@ def test_product_matches_64_bits(pq, m, n, k, block):
 
 @pytest.mark.parametrize("out", ["fp32", "fp16"])
 @pytest.mark.parametrize("block", [R.TILE, R.ROW])
-@pytest.mark.parametrize("m,n,k", [(1, 300, 700), (33, 129, 128), (260, 390, 1290), (1100, 2056, 520)])
+@pytest.mark.parametrize("m,n,k", [(1, 300, 700), (33, 129, 128), (260, 390, 1290), (1100, 2056, 520), (2000, 2047, 260)])
 def test_product_output_types(pq, m, n, k, block, out):
     check_product(pq, m, n, k, block, out, seed=m, std=0.05)
 
