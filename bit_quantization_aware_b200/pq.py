@@ -187,6 +187,8 @@ def _declare(L):
 def lib(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load the CUDA library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -210,8 +212,14 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# the current stream without a Stream object around it (3 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -569,15 +577,18 @@ def clip_grad_norm(tensors, max_norm, stream=None):
 # --------------------------------------------- e4m3 blocks and their product
 def _pitch(t, name, dtypes):
     """(pointer, row pitch in elements) of a matrix whose rows are contiguous."""
-    if t.dim() != 2 or t.dtype not in dtypes:
+    shape = t.shape
+    if len(shape) != 2 or t.dtype not in dtypes:
         raise ValueError(f"{name} must be a matrix of {' or '.join(map(str, dtypes))}")
     if not t.is_cuda:
         raise ValueError("expected a CUDA tensor")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = shape
+    pitch, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    # a matrix of one row may carry any pitch
-    pitch = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-    if pitch < t.shape[1]:
+    if rows <= 1 and pitch < cols:  # a matrix of one row may carry any pitch
+        pitch = cols
+    if pitch < cols:
         raise ValueError(f"{name} must have rows that do not overlap")
     return t.data_ptr(), pitch
 
@@ -602,7 +613,7 @@ def fp8_scale_shape(block, rows, cols):
 
 
 def _scales(s, block, rows, cols, name):
-    if s.dtype != torch.float32 or tuple(s.shape) != fp8_scale_shape(block, rows, cols):
+    if s.dtype is not torch.float32 or s.shape != fp8_scale_shape(block, rows, cols):
         raise ValueError(f"{name} must be fp32 {list(fp8_scale_shape(block, rows, cols))}")
     return _ptr(s)
 
@@ -611,16 +622,17 @@ def pq_fp8_quant(block, x, q_out=None, s_out=None, qt_out=None, st_out=None, str
     """e4m3 codes and scales of x (bf16, fp16 or fp32 [rows, cols]): ``q_out``
     [rows, cols] with ``s_out``, and/or those of its transpose: ``qt_out``
     [cols, rows] with ``st_out`` (shapes: ``fp8_scale_shape``)."""
-    xp, ldx = _pitch(x, "x", tuple(DTYPES))
+    xp, ldx = _pitch(x, "x", DTYPES)
     rows, cols = x.shape
     args = []
     for q, s, r, c, name in ((q_out, s_out, rows, cols, "q_out"), (qt_out, st_out, cols, rows, "qt_out")):
         if q is None:
-            args += [None, 0, None]
+            args += (None, 0, None)
             continue
-        if tuple(q.shape) != (r, c) or s is None:
+        if q.shape != (r, c) or s is None:
             raise ValueError(f"{name} must be [{r}, {c}], with its scales")
-        args += [*_pitch(q, name, _CODES), _scales(s, block, r, c, "scales of " + name)]
+        args += _pitch(q, name, _CODES)
+        args.append(_scales(s, block, r, c, "scales of " + name))
     _check("pq_fp8_quant", lib().pq_fp8_quant(
         block, DTYPES[x.dtype], rows, cols, xp, ldx, *args, _stream(stream)))
 
@@ -653,9 +665,10 @@ def pq_fp8_gemm(a, a_scale, b, b_scale, b_block, y_out, stream=None):
     b [n, k] with ``b_block`` blocks, y_out bf16, fp16 or fp32 [m, n]."""
     ap, lda = _pitch(a, "a", _CODES)
     bp, ldb = _pitch(b, "b", _CODES)
-    yp, ldy = _pitch(y_out, "y_out", tuple(DTYPES))
-    (m, k), n = a.shape, b.shape[0]
-    if b.shape[1] != k or tuple(y_out.shape) != (m, n):
+    yp, ldy = _pitch(y_out, "y_out", DTYPES)
+    m, k = a.shape
+    n, kb = b.shape
+    if kb != k or y_out.shape != (m, n):
         raise ValueError("pq_fp8_gemm: shapes must be a [m, k], b [n, k], y_out [m, n]")
     _check("pq_fp8_gemm", lib().pq_fp8_gemm(
         m, n, k, ap, lda, _scales(a_scale, PQ_BLOCK_ROW, m, k, "a_scale"), bp, ldb,
