@@ -15,7 +15,11 @@
 // same bits on every run; every CTA leaves one partial sum in the workspace,
 // and the kernel that follows adds those in a fixed order (no atomics).
 //
-// Bound: memory. The norm reads each gradient once; scaling reads and writes
+// Bound: memory. fp64 itself has the rate for it, the conversion unit has not
+// (fp32 to fp64 conversions kept it 76% busy at 5.0 TB/s of bf16 gradients):
+// tensors are widened with integer operations instead, see widen, and the
+// quantizer's dW, zero or g, is not converted a second time.
+// The norm reads each gradient once; scaling reads and writes
 // it once more, from the last unit to the first, so what the norm pass left
 // in L2 is read there. An in-place scale with coef == 1 touches nothing.
 #include <cuda_bf16.h>
@@ -24,6 +28,8 @@
 
 #include <math.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "pq.h"
 #include "pq_launches.cuh"
@@ -57,6 +63,40 @@ template <>
 __device__ __forceinline__ __nv_bfloat16 from_float(float v) { return __float2bfloat16_rn(v); }
 template <>
 __device__ __forceinline__ __half from_float(float v) { return __float2half_rn(v); }
+
+// |v| as fp64 times 2^-896, from fp32 bits: the exponent field moves as it is
+// (fp64's bias is 896 more), so zeros and subnormals come out right, and 2^896
+// times it is |v| exactly. Inf and NaN come out finite; Special keeps them.
+__device__ __forceinline__ double widen(uint32_t bits) {
+    return __hiloint2double(static_cast<int>((bits & 0x7FFFFFFFu) >> 3), static_cast<int>(bits << 29));
+}
+constexpr double kWiden = 0x1p896;
+
+__device__ __forceinline__ double add_square(uint32_t bits, double acc) {
+    const double e = __dmul_rn(widen(bits), kWiden);
+    return __fma_rn(e, e, acc);
+}
+
+// The largest magnitude that a thread met, as ordered bits of T (two 16-bit
+// values a word): NaN above Inf above every finite value.
+template <typename T>
+struct Special {
+    uint32_t m = 0;
+    __device__ __forceinline__ void see(uint32_t word) {
+        if constexpr (sizeof(T) == 2) m = __vmaxu2(m, word & 0x7FFF7FFFu);
+        else m = max(m, word & 0x7FFFFFFFu);
+    }
+    // the thread's sum: NaN or Inf if it met one
+    __device__ __forceinline__ double close(double acc) const {
+        uint32_t v = m, inf = 0x7F800000u;
+        if constexpr (sizeof(T) == 2) {
+            v = max(v & 0xFFFFu, v >> 16);
+            inf = std::is_same_v<T, __half> ? 0x7C00u : 0x7F80u;
+        }
+        if (v < inf) return acc;
+        return __hiloint2double(v == inf ? 0x7FF00000 : 0x7FFFFFFF, 0);
+    }
+};
 
 // One 32-byte vector of T (8 or 16 elements).
 template <typename T>
@@ -111,6 +151,20 @@ __device__ __forceinline__ float clip_coef(double norm, double max_norm) {
     return c >= 1.0 ? 1.0f : static_cast<float>(c);
 }
 
+// The entry that owns unit u, by bisection: a CTA's first unit may lie behind
+// hundreds of entries, whose descriptors it would otherwise read one by one
+// (98 tensors of 2048 elements: 12.9 us for the norm and the scaling so).
+template <typename D, int CAP>
+__device__ __forceinline__ int locate(const BatchT<D, CAP>& b, int64_t u) {
+    int lo = 0, hi = b.n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (b.m[mid].unit_begin <= u) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
 // ----------------------------------------------------------------- tensors
 struct TensorDesc {
     const void* g;
@@ -132,8 +186,9 @@ __global__ void __launch_bounds__(kThreads)
 norm_tensors_kernel(const __grid_constant__ NormBatch<T, CAP> P) {
     constexpr int kUnit = kUnitBytes / sizeof(T);
     constexpr int V = Vec<T>::kN;
-    double acc = 0.0;
-    int mi = 0;
+    double acc[2] = {0.0, 0.0};
+    Special<T> special;
+    int mi = locate(P.b, blockIdx.x);
     for (int64_t u = blockIdx.x; u < P.b.total_units; u += gridDim.x) {
         mi = find_matrix(P.b, mi, u);
         const TensorDesc& t = P.b.m[mi];
@@ -154,20 +209,30 @@ norm_tensors_kernel(const __grid_constant__ NormBatch<T, CAP> P) {
                 const int at = (k * kThreads + static_cast<int>(threadIdx.x)) * V;
                 if (at < done) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const double e = static_cast<double>(to_float(v[k].e[i]));
-                        acc = __fma_rn(e, e, acc);
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t w = v[k].w[i];
+                        special.see(w);
+                        if constexpr (std::is_same_v<T, float>) {
+                            acc[i & 1] = add_square(w, acc[i & 1]);
+                        } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+                            acc[0] = add_square(w << 16, acc[0]);
+                            acc[1] = add_square(w & 0xFFFF0000u, acc[1]);
+                        } else {
+                            acc[0] = add_square(__float_as_uint(to_float(v[k].e[2 * i])), acc[0]);
+                            acc[1] = add_square(__float_as_uint(to_float(v[k].e[2 * i + 1])), acc[1]);
+                        }
                     }
                 }
             }
         }
         for (int i = done + static_cast<int>(threadIdx.x); i < n; i += kThreads) {
-            const double e = static_cast<double>(to_float(g[i]));
-            acc = __fma_rn(e, e, acc);
+            if constexpr (sizeof(T) == 2) special.see(reinterpret_cast<const uint16_t*>(g)[i]);
+            else special.see(reinterpret_cast<const uint32_t*>(g)[i]);
+            acc[0] = add_square(__float_as_uint(to_float(g[i])), acc[0]);
         }
     }
-    acc = block_sum(acc);
-    if (threadIdx.x == 0) P.partial[blockIdx.x] = acc;
+    const double sum = block_sum(special.close(__dadd_rn(acc[0], acc[1])));
+    if (threadIdx.x == 0) P.partial[blockIdx.x] = sum;
 }
 
 // What closes a norm: the partial sums of its launches and where the results go.
@@ -220,7 +285,7 @@ scale_tensors_kernel(const __grid_constant__ ScaleBatch<T, O, CAP> P) {
     }
     __syncthreads();
     const float c = s_coef;
-    int mi = P.b.n - 1;
+    int mi = locate(P.b, P.b.total_units - 1 - blockIdx.x);
     for (int64_t r = blockIdx.x; r < P.b.total_units; r += gridDim.x) {
         const int64_t u = P.b.total_units - 1 - r;
         while (P.b.m[mi].unit_begin > u) --mi;
@@ -266,6 +331,23 @@ scale_tensors_kernel(const __grid_constant__ ScaleBatch<T, O, CAP> P) {
 // gradients, as in pq_reduce_bwd_adamw.
 constexpr int kMaxSources = 16;
 
+// One chunk: the row's d(alpha) sum as bwd_chunk forms it, and the squares of
+// dW from the same widened g.
+template <int Q>
+__device__ __forceinline__ void norm_chunk(const float (&v)[8], const float (&g)[8], const RowScale& s,
+                                           double& acc, double& sq) {
+    float x[8];
+    divide8(v, s, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const Elem e = quantize_x<Q>(x[i]);
+        const float xm = e.inside ? x[i] : 0.0f;
+        const double dg = static_cast<double>(g[i]);
+        acc = __fma_rn(dg, __dsub_rn(static_cast<double>(e.level), static_cast<double>(xm)), acc);
+        if (e.inside) sq = __fma_rn(dg, dg, sq);
+    }
+}
+
 struct GradDesc {
     const float* w;
     const float* alpha;
@@ -293,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, PQ_BWD_MIN_CTAS)
 norm_matrices_kernel(const __grid_constant__ GradBatch<CAP> P) {
     __shared__ double warp_sum[2][kThreads / 32];
     double sq = 0.0;
-    int mi = 0, prev_mi = 0, parity = 0;
+    int mi = locate(P.b, blockIdx.x), prev_mi = mi, parity = 0;
     // block-uniform trip count: every thread reaches every barrier
     for (int64_t u = blockIdx.x; u < P.b.total_units; u += gridDim.x, parity ^= 1) {
         mi = find_matrix(P.b, mi, u);
@@ -337,10 +419,9 @@ norm_matrices_kernel(const __grid_constant__ GradBatch<CAP> P) {
                 for (int k = 0; k < U; ++k) {
                     const int64_t c = ch + k * tpr;
                     if (c >= nch) continue;
-                    float d[8];
+                    float gs[8];
                     if constexpr (SHARD) {
                         const int n = tail_n(m.cols, c);
-                        float gs[8];
                         if constexpr (VEC) load8(wr + c * 8, v[k]);
                         else load8_tail(wr + c * 8, n, v[k]);
 #pragma unroll
@@ -356,15 +437,13 @@ norm_matrices_kernel(const __grid_constant__ GradBatch<CAP> P) {
                         }
 #pragma unroll
                         for (int i = 0; i < 8; ++i) gs[i] = __fmul_rn(gs[i], P.grad_mult);
-                        acc = bwd_chunk_f32<Q>(v[k], gs, a, d, acc);
                     } else {
-                        acc = bwd_chunk<Q>(v[k], gw[k], a, d, acc);
-                    }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const double e = static_cast<double>(d[i]);
-                        sq = __fma_rn(e, e, sq);
+                        for (int i = 0; i < 8; ++i)
+                            gs[i] = (i & 1) ? __uint_as_float(gw[k][i / 2] & 0xFFFF0000u)
+                                            : __uint_as_float(gw[k][i / 2] << 16);
                     }
+                    norm_chunk<Q>(v[k], gs, a, acc, sq);
                 }
             }
         }
