@@ -793,16 +793,21 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
             if (k0 >= k1) return true;
             fetch(k0, a0);
             fetch(k0 + 1, a1);
+            uint32_t ready = 0;
             auto block = [&](int kb, float(&next)[4]) -> bool {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) a[i] = next[i];
                 fetch(kb + 2, next);
-                if (!uniform_wait<false>(b_sfull + 8u * sr.idx, sr.phase, abort) ||
-                    !uniform_wait<false>(dfull + 8u * d.idx, d.phase, abort))
+                if (!__any_sync(0xFFFFFFFFu, ready) &&
+                    (!uniform_wait<false>(b_sfull + 8u * sr.idx, sr.phase, abort) ||
+                     !uniform_wait<false>(dfull + 8u * d.idx, d.phase, abort)))
                     return false;
                 tc_fence_after();
                 const float* bs = scales + sr.idx * NT + part * C + 2 * (lane % 4);
                 const uint32_t src = buffer();
+                const uint32_t free_bar = dempty + 8u * d.idx, free_scales = b_sempty + 8u * sr.idx;
+                d.next();
+                sr.next();
                 uint32_t v[2][16];  // 32 columns of 16 rows: reads run one ahead
                 tmem_ld_rows(src, v[0]);
 #pragma unroll
@@ -815,7 +820,10 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
                         tmem_wait(v[g]);
                         if (g == 0) tmem_ld_rows(src + c + (16u << 16), v[1]);
                         else if (c + 32 < C) tmem_ld_rows(src + c + 32, v[0]);
-                        else free_buffer(dempty + 8u * d.idx);
+                        else free_buffer(free_bar);
+                        if (g == 1 && c + 64 == C)
+                            ready = mbar_test<false>(b_sfull + 8u * sr.idx, sr.phase) &
+                                    mbar_test<false>(dfull + 8u * d.idx, d.phase);
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -828,9 +836,7 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
                     }
                 }
                 __syncwarp();
-                mbar_arrive_if(b_sempty + 8u * sr.idx, one);
-                sr.next();
-                d.next();
+                mbar_arrive_if(free_scales, one);
                 return true;
             };
             for (int kb = k0; kb < k1; kb += 2) {

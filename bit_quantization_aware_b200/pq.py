@@ -212,8 +212,14 @@ def _ptr(t):
     return t.data_ptr()
 
 
-# the current stream without a Stream object around it (3 us a call)
+# the current device and stream without objects around them (3 us a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _current_device() -> int:
+    if _raw_stream is not None and torch.cuda.is_initialized():
+        return torch._C._cuda_getDevice()
+    return torch.cuda.current_device()
 
 
 def _stream(stream):
@@ -465,6 +471,21 @@ def pq_wq_gemm_noalloc(q, x, packed, alpha, y_out, stream=None):
     _check("pq_wq_gemm_noalloc", status)
 
 
+def _one_device(*tensors):
+    """The tensors' device index; raises unless they share one and it is the
+    current device, whose stream and context the kernels run in."""
+    found = {t if isinstance(t, int) else t.get_device() for t in tensors if t is not None}
+    found.discard(-1)
+    if not found:
+        return -1
+    if len(found) > 1:
+        raise ValueError("tensors on different devices: " + ", ".join(f"cuda:{d}" for d in sorted(found)))
+    dev = found.pop()
+    if dev != _current_device():
+        raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{_current_device()}")
+    return dev
+
+
 # ------------------------------------------------- gradient norm and clipping
 def _one(t, dtype, name):
     """Pointer of a one-element device tensor (None passes as NULL)."""
@@ -492,6 +513,7 @@ def tensor_array(tensors, outs=None):
     if len(outs) != len(tensors):
         raise ValueError("outs must have one entry for each tensor")
     arr = (PQTensor * len(tensors))()
+    arr.device_index = _one_device(*tensors, *outs)
     written = set()
     for d, t, o in zip(arr, tensors, outs):
         if t.dtype not in DTYPES:
@@ -518,6 +540,7 @@ def pq_grad_norm(max_norm, norm_out, coef_out, workspace, tensors=None, q=0, mat
     clipping factor min(1, max_norm / (norm + 1e-6)). Outputs are device
     tensors of one element: fp32 ``norm_out``, ``coef_out``, fp64
     ``sumsq_out``; each may be None, not all."""
+    _one_device(workspace, norm_out, coef_out, sumsq_out, getattr(tensors, "device_index", None))
     ws, ws_bytes = _workspace(workspace)
     _check("pq_grad_norm", lib().pq_grad_norm(
         0 if tensors is None else len(tensors), tensors, q, 0 if mats is None else len(mats), mats,
@@ -542,6 +565,7 @@ def pq_clip_coef(sumsq, max_norm, norm_out, coef_out, stream=None):
     device), e.g. every rank's ``sumsq_out``."""
     if sumsq.dtype != torch.float64:
         raise ValueError("sumsq must be fp64")
+    _one_device(sumsq, norm_out, coef_out)
     _check("pq_clip_coef", lib().pq_clip_coef(
         sumsq.numel(), _ptr(sumsq), max_norm, _f32_1(norm_out, "norm_out"),
         _f32_1(coef_out, "coef_out"), _stream(stream)))
@@ -549,12 +573,14 @@ def pq_clip_coef(sumsq, max_norm, norm_out, coef_out, stream=None):
 
 def pq_grad_scale(tensors, coef, stream=None):
     """Every tensor of a ``pq_tensor_t[]`` times the device factor ``coef``."""
+    _one_device(coef, getattr(tensors, "device_index", None))
     _check("pq_grad_scale", lib().pq_grad_scale(
         len(tensors), tensors, _f32_1(coef, "coef"), _stream(stream)))
 
 
 def pq_grad_clip(tensors, max_norm, norm_out, coef_out, workspace, stream=None):
     """Clips a ``pq_tensor_t[]`` by its global norm."""
+    _one_device(workspace, norm_out, coef_out, getattr(tensors, "device_index", None))
     ws, ws_bytes = _workspace(workspace)
     _check("pq_grad_clip", lib().pq_grad_clip(
         len(tensors), tensors, max_norm, _f32_1(norm_out, "norm_out"),
@@ -623,6 +649,7 @@ def pq_fp8_quant(block, x, q_out=None, s_out=None, qt_out=None, st_out=None, str
     [rows, cols] with ``s_out``, and/or those of its transpose: ``qt_out``
     [cols, rows] with ``st_out`` (shapes: ``fp8_scale_shape``)."""
     xp, ldx = _pitch(x, "x", DTYPES)
+    _one_device(x, q_out, s_out, qt_out, st_out)
     rows, cols = x.shape
     args = []
     for q, s, r, c, name in ((q_out, s_out, rows, cols, "q_out"), (qt_out, st_out, cols, rows, "qt_out")):
@@ -666,6 +693,7 @@ def pq_fp8_gemm(a, a_scale, b, b_scale, b_block, y_out, stream=None):
     ap, lda = _pitch(a, "a", _CODES)
     bp, ldb = _pitch(b, "b", _CODES)
     yp, ldy = _pitch(y_out, "y_out", DTYPES)
+    _one_device(a, a_scale, b, b_scale, y_out)
     m, k = a.shape
     n, kb = b.shape
     if kb != k or y_out.shape != (m, n):

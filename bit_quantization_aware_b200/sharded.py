@@ -19,7 +19,9 @@ step, per GPU:
    ``reduce_step``: each GPU sums every replica's gradient rows of the
    shards it owns (fp32, fixed replica order, times 1/world) and applies
    the STE backward, d(alpha) and AdamW to them, in one kernel
-   (the reduce-scatter is fused into the backward).
+   (the reduce-scatter is fused into the backward). With a largest norm given,
+   a pass over the same gradients forms their global norm first and the update
+   clips by it; one fp64 number a rank is exchanged.
 
 Ordering: ``forward`` and ``backward`` put the caller's barrier between the
 phases (pack -> barrier -> gather; the model writes the gradient ->
@@ -217,6 +219,7 @@ class ShardedQuantStep:
         self.m_a = torch.zeros(nr, dtype=torch.float32, device=dev)
         self.v_a = torch.zeros(nr, dtype=torch.float32, device=dev)
         self.dalpha = torch.zeros(nr, dtype=torch.float32, device=dev)
+        self._clip = None  # buffers of clip_coef, from its first call
 
     # ---------------------------------------------------------- views
     def my_rows(self, i):
@@ -273,7 +276,8 @@ class ShardedQuantStep:
                                   wq=self.wq_full[e0 + b * m.cols:e0 + e * m.cols]))
         self.lib.pq_dequant_codes_batch(self.q, self.lib.matrix_array(descs), stream)
 
-    def reduce_step(self, hp_w, hp_alpha, grad_mult=None, stream=None):
+    def _reduce_args(self, grad_mult):
+        """(sources, factor, shard descriptors) of this rank's reductions."""
         sources = [self.peers.get(k, "g") for k in range(self.world)]
         shards = []
         for i, m in enumerate(self.mats):
@@ -290,8 +294,35 @@ class ShardedQuantStep:
                                dalpha=self.dalpha[r0 + b:r0 + e], g_offset=e0 + b * m.cols,
                                grad_scale=self.lib.pq_default_grad_scale(self.q, m.cols)))
         mult = 1.0 / self.world if grad_mult is None else grad_mult
-        self.lib.pq_reduce_bwd_adamw(self.q, sources, mult, self.lib.shard_array(shards), hp_w,
-                                     hp_alpha, stream)
+        return sources, mult, self.lib.shard_array(shards)
+
+    def reduce_step(self, hp_w, hp_alpha, grad_mult=None, stream=None, coef=None):
+        """Reduce + backward + AdamW on the owned shards; ``coef`` (fp32 [1],
+        from ``clip_coef``) clips the gradients."""
+        sources, mult, shards = self._reduce_args(grad_mult)
+        clip = {} if coef is None else {"coef": coef}
+        self.lib.pq_reduce_bwd_adamw(self.q, sources, mult, shards, hp_w, hp_alpha, stream, **clip)
+
+    def clip_coef(self, max_norm, gather=None, grad_mult=None, stream=None):
+        """(norm, factor), fp32 [1] each, of the whole step's reduced
+        gradients: this rank's shards add their squares, ``gather`` (fp64 [1]
+        of this rank -> fp64 [world] of all, ordered with the stream like the
+        barrier; not needed for one rank) collects the ranks' sums, and every
+        rank adds them in the same order, so all clip alike."""
+        if gather is None and self.world > 1:
+            raise ValueError("clip_coef needs a gather over the ranks' sums")
+        sources, mult, shards = self._reduce_args(grad_mult)
+        if self._clip is None:  # workspace, sum of squares, norm, factor
+            dev = self.device
+            self._clip = (torch.empty(self.lib.pq_grad_norm_workspace_bytes(0, len(self.mats)),
+                                      dtype=torch.uint8, device=dev),
+                          torch.zeros(1, dtype=torch.float64, device=dev),
+                          torch.zeros(1, device=dev), torch.zeros(1, device=dev))
+        ws, sumsq, norm, coef = self._clip
+        self.lib.pq_reduce_grad_norm(self.q, sources, mult, shards, max_norm, None, None, ws,
+                                     sumsq_out=sumsq, stream=stream)
+        self.lib.pq_clip_coef(sumsq if gather is None else gather(sumsq), max_norm, norm, coef, stream)
+        return norm, coef
 
     # ---------------------------------------------------------- one step
     def forward(self, barrier, stream=None):
@@ -302,10 +333,18 @@ class ShardedQuantStep:
         barrier()
         self.gather_dequant(stream)
 
-    def backward(self, barrier, hp_w, hp_alpha, grad_mult=None, stream=None):
+    def backward(self, barrier, hp_w, hp_alpha, grad_mult=None, stream=None, max_norm=None,
+                 gather=None):
         """Backward of one step, after the model wrote this rank's full
         upstream gradient into ``g``: wait at ``barrier`` until every
         rank's gradient is written, then reduce + backward + AdamW on the
-        owned shards."""
+        owned shards. With ``max_norm`` the gradients are clipped by the
+        global norm first (``gather``: see ``clip_coef``); returns that norm
+        (fp32 [1]), else None."""
         barrier()
-        self.reduce_step(hp_w, hp_alpha, grad_mult, stream)
+        if max_norm is None:
+            self.reduce_step(hp_w, hp_alpha, grad_mult, stream)
+            return None
+        norm, coef = self.clip_coef(max_norm, gather, grad_mult, stream)
+        self.reduce_step(hp_w, hp_alpha, grad_mult, stream, coef)
+        return norm

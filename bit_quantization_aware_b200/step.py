@@ -89,6 +89,8 @@ class QuantStep:
                  dw=b.dw, dalpha=b.dalpha, grad_scale=b.grad_scale)
             for b in self.bufs])
 
+        self._norm, self._clip_descs = {}, None
+
     @property
     def weights(self) -> int:
         return sum(m.numel for m in self.mats)
@@ -130,6 +132,33 @@ class QuantStep:
         for b in self.bufs:
             pq.pq_fakequant_bwd(self.q, b.w, b.alpha, b.g, b.dw, b.dalpha,
                                 b.grad_scale, stream)
+
+    def _norm_buffers(self, n):
+        """Workspace for n entries, norm and factor (kept: a captured call
+        goes on using them)."""
+        if n not in self._norm:
+            dev = self.device
+            self._norm[n] = (torch.empty(pq.pq_grad_norm_workspace_bytes(n, n), dtype=torch.uint8, device=dev),
+                             torch.zeros(1, device=dev), torch.zeros(1, device=dev))
+        return self._norm[n]
+
+    def grad_norm(self, max_norm, stream=None):
+        """(norm, clipping factor), fp32 [1] each, of the quantizer gradients
+        of every matrix, formed from w, alpha and g without dW: the factor is
+        what ``pq_fakequant_bwd_adamw`` takes as ``coef``."""
+        ws, norm, coef = self._norm_buffers(len(self.bufs))
+        pq.pq_grad_norm(max_norm, norm, coef, ws, q=self.q, mats=self._bwd_descs, stream=stream)
+        return norm, coef
+
+    def clip_grads(self, max_norm, stream=None):
+        """Clips the dW and d(alpha) that ``bwd_all`` wrote by their global
+        norm, in place; returns the norm before it (fp32 [1])."""
+        if self._clip_descs is None:
+            self._clip_descs = pq.tensor_array([t for b in self.bufs if b.m.rows
+                                                for t in ((b.dw, b.dalpha) if b.m.cols else (b.dalpha,))])
+        ws, norm, coef = self._norm_buffers(len(self._clip_descs))
+        pq.pq_grad_clip(self._clip_descs, max_norm, norm, coef, ws, stream)
+        return norm
 
     def run(self, stream=None):
         self.fwd_all(stream)

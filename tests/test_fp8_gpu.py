@@ -209,16 +209,40 @@ def test_another_stream_and_graph_replay(pq):
     x.mul_(0.25)
 
 
+def test_two_streams_at_once(pq):
+    """Calls share no state: products and quantizations that overlap on the
+    GPU give what they give alone."""
+    sets = []
+    for i, (m, n, k, block) in enumerate([(700, 1500, 1100, R.TILE), (5, 640, 3000, R.ROW), (2000, 2050, 300, R.ROW)]):
+        x, w = draw(m, k, i, torch.bfloat16).to(DEV), draw(n, k, i + 9, torch.bfloat16).to(DEV)
+        b, sb, _, _ = pq.fp8_quant(w, block)
+        q, s, _, _ = pq.fp8_quant(x, R.ROW)
+        sets.append((x, q, s, b, sb, block, pq.fp8_gemm(q, s, b, sb, block)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    outs = [[] for _ in sets]
+    for _ in range(8):
+        for st, (x, q, s, b, sb, block, _), o in zip(streams, sets, outs):
+            with torch.cuda.stream(st):
+                q2, s2, _, _ = pq.fp8_quant(x, R.ROW)
+                o.append(pq.fp8_gemm(q2, s2, b, sb, block))
+    torch.cuda.synchronize()
+    for o, (*_, want) in zip(outs, sets):
+        assert all(torch.equal(y, want) for y in o)
+
+
 def test_waits_give_up_with_a_status(pq):
-    a, sa, b, sb, y = check_product(pq, 40, 300, 1024, R.ROW, "bf16")
-    pq.pq_debug_abort_waits(True)
-    try:
-        pq.fp8_gemm(a, sa, b, sb, R.ROW)
-        assert pq.pq_device_status() == pq.PQ_ERR_TIMEOUT
-    finally:
-        pq.pq_debug_abort_waits(False)
-    assert pq.pq_device_status() == pq.PQ_OK
-    assert torch.equal(pq.fp8_gemm(a, sa, b, sb, R.ROW), y)
+    for m, n, k, block in ((40, 300, 1024, R.ROW), (33, 4096, 520, R.TILE), (1100, 2056, 520, R.TILE),
+                           (1100, 2056, 520, R.ROW)):
+        a, sa, b, sb, y = check_product(pq, m, n, k, block, "bf16")
+        pq.pq_debug_abort_waits(True)
+        try:
+            pq.fp8_gemm(a, sa, b, sb, block)
+            assert pq.pq_device_status() == pq.PQ_ERR_TIMEOUT
+        finally:
+            pq.pq_debug_abort_waits(False)
+        assert pq.pq_device_status() == pq.PQ_OK
+        assert torch.equal(pq.fp8_gemm(a, sa, b, sb, block), y)
 
 
 # --------------------------------------------------------- the linear layer

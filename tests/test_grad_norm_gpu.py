@@ -420,3 +420,63 @@ def test_a_training_step_together(pq):
     assert torch.equal(st["m_w"], 0.9 * m0 + np.float32(1 - 0.9) * (dw * coef)) or \
         torch.allclose(st["m_w"], 0.9 * m0 + (1 - 0.9) * (dw * coef), rtol=2 ** -21, atol=1e-12)
     assert not torch.equal(st["w"], w0)
+
+
+@pytest.mark.parametrize("world", [1, 2])
+def test_sharded_step_clips_like_the_unsharded(pq, world):
+    from bit_quantization_aware_b200.sharded import LocalPeers, ShardedQuantStep
+    mats = [I.Matrix("a", 300, 256, 0, 0), I.Matrix("b", 7, 40, 0, 1), I.Matrix("one", 1, 64, 0, 2)]
+    q = pq.PQ_LSQ4
+    peers = LocalPeers(world)
+    ranks = [ShardedQuantStep(mats, q, k, world, peers, device=DEV) for k in range(world)]
+    one = []
+    for i, m in enumerate(mats):
+        w = I.normal_weights(m.rows, m.cols, seed=i, stream=0, device=DEV)
+        a = I.alpha_init(w, q)
+        g = I.grad_bf16(m.rows, m.cols, seed=9, stream=i, device=DEV)
+        for r in ranks:
+            r.load_full(i, w, a)
+            r.g(i).copy_(g)  # equal replicas: their mean is g
+        z = lambda *s: torch.zeros(*s, device=DEV)
+        one.append(dict(rows=m.rows, cols=m.cols, w=w.clone(), alpha=a.clone(), g=g, m_w=z(m.rows, m.cols),
+                        v_w=z(m.rows, m.cols), m_alpha=z(m.rows), v_alpha=z(m.rows),
+                        grad_scale=pq.pq_default_grad_scale(q, m.cols)))
+    hw, ha = pq.adamw(1, 1e-4), pq.adamw(1, 1e-5)
+    norm, coef = outs()
+    pq.pq_grad_norm(0.01, norm, coef, scratch(pq, 0, len(one)), q=q, mats=pq.matrix_array(one))
+    pq.pq_fakequant_bwd_adamw(q, pq.adamw_matrix_array(one), hw, ha, coef=coef)
+    sums = torch.zeros(world, dtype=torch.float64, device=DEV)
+    for r in ranks:  # every rank's sum before any rank's update
+        sources, mult, shards = r._reduce_args(None)
+        pq.pq_reduce_grad_norm(q, sources, mult, shards, 0.01, None, None, scratch(pq, 0, len(mats)),
+                               sumsq_out=sums[r.rank:r.rank + 1])
+    for r in ranks:
+        got, c = r.clip_coef(0.01, gather=lambda s: sums)
+        # both add the same squares, in another order
+        assert float(got) == pytest.approx(float(norm), rel=RTOL)
+        assert float(c) == pytest.approx(float(coef), rel=RTOL)
+        r.reduce_step(hw, ha, coef=coef)
+    for i, m in enumerate(mats):
+        for r in ranks:
+            b, e = r.my_rows(i)
+            assert torch.equal(r.w_shard(i), one[i]["w"][b:e])
+            assert torch.equal(r.alpha_rows(i, b, e), one[i]["alpha"][b:e])
+
+
+def test_quant_step_norm_and_clip(pq):
+    from bit_quantization_aware_b200.step import QuantStep
+    mats = [I.Matrix("a", 256, 512, 0, 0), I.Matrix("b", 33, 72, 0, 1)]
+    st = QuantStep(mats, pq.PQ_SEQ2, device=DEV)
+    st.generate(seed=3)
+    st.run()
+    grads = [t.clone() for b in st.bufs for t in (b.dw, b.dalpha)]
+    want = norm64(grads)
+    norm, coef = st.grad_norm(0.25 * want)
+    assert float(norm) == pytest.approx(want, rel=RTOL)
+    assert float(coef) == pytest.approx(coef_of(want, 0.25 * want), rel=RTOL)
+    c = coef.clone()
+    norm = st.clip_grads(0.25 * want)
+    assert float(norm) == pytest.approx(want, rel=RTOL)
+    for t, k in zip([t for b in st.bufs for t in (b.dw, b.dalpha)], grads):
+        # the two norms may round differently: factors within an fp32 step
+        assert torch.allclose(t, k * c, rtol=2.0 ** -22, atol=0)

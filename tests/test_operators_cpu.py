@@ -188,6 +188,36 @@ def test_binding_refusals(pq):
         pq.pq_fp8_gemm(FakeCuda(torch.zeros(1, 32, dtype=u8).expand(4, 32)), m(1, 4), m(8, 32, u8), m(1, 1), 2, m(4, 8))
 
 
+def test_tensors_of_another_device_are_refused(pq, monkeypatch):
+    """One device a call, and the current one: its stream launches."""
+    class On(FakeCuda):
+        def __init__(self, dev, *shape, dtype=torch.float32):
+            super().__init__(torch.zeros(*shape, dtype=dtype))
+            self.dev = dev
+
+        def get_device(self):
+            return self.dev
+
+    monkeypatch.setattr(pq, "_current_device", lambda: 0)
+    u8 = torch.uint8
+    for a, b, word in ((0, 1, "different devices"), (1, 1, "current device is cuda:0")):
+        with pytest.raises(ValueError, match=word):
+            pq.pq_fp8_gemm(On(a, 4, 32, dtype=u8), On(b, 1, 4), On(b, 8, 32, dtype=u8), On(b, 1, 1), 2, On(b, 4, 8))
+        with pytest.raises(ValueError, match=word):
+            pq.pq_fp8_quant(1, On(a, 4, 8), On(b, 4, 8, dtype=u8), On(b, 1, 4))
+        with pytest.raises(ValueError, match=word):
+            pq.tensor_array([On(a, 8), On(b, 8)])
+        with pytest.raises(ValueError, match=word):
+            pq.pq_clip_coef(On(a, 1, dtype=torch.float64), 1.0, On(b, 1), On(b, 1))
+    arr = pq.tensor_array([On(0, 8)])
+    with pytest.raises(ValueError, match="different devices"):
+        pq.pq_grad_clip(arr, 1.0, On(1, 1), None, On(1, 64, dtype=u8))
+    with pytest.raises(ValueError, match="different devices"):
+        pq.pq_grad_scale(arr, On(1, 1))
+    with pytest.raises(ValueError, match="different devices"):
+        pq.pq_grad_norm(1.0, On(1, 1), None, On(1, 64, dtype=u8), tensors=arr)
+
+
 def test_linear_refusals(pq, monkeypatch):
     from bit_quantization_aware_b200.linear import Fp8Linear
     monkeypatch.setattr(pq, "pq_fp8_quant", lambda *a: None)
