@@ -448,12 +448,15 @@ struct AdamDesc {
     int32_t tpr_log2;
 };
 
-struct AdamBatch {
-    BatchT<AdamDesc> b;
+template <int CAP>
+struct AdamBatchT {
+    BatchT<AdamDesc, CAP> b;
     AdamK kw;  // weights
     AdamK ka;  // scales
     const float* coef;  // gradient clipping factor (NULL: 1)
 };
+
+using AdamBatch = AdamBatchT<kMaxBatch>;
 
 // The factor every gradient is multiplied by before its AdamW step; times 1
 // no value changes.
@@ -461,10 +464,10 @@ __device__ __forceinline__ float grad_coef(const float* coef) {
     return coef ? __ldg(coef) : 1.0f;
 }
 
-template <int Q, bool VEC>
+template <int Q, bool VEC, int CAP>
 __global__ void __launch_bounds__(kThreads, 3)
-bwd_adamw_units_kernel(const __grid_constant__ AdamBatch P) {
-    const BatchT<AdamDesc>& p = P.b;
+bwd_adamw_units_kernel(const __grid_constant__ AdamBatchT<CAP> P) {
+    const BatchT<AdamDesc, CAP>& p = P.b;
     __shared__ double warp_sum[2][kThreads / 32];
     const float coef = grad_coef(P.coef);
     int mi = 0, prev_mi = 0, parity = 0;
@@ -985,14 +988,29 @@ static bool adamw_ok(const pq_adamw_t* h) {
            h->beta2 < 1.0 && h->eps > 0.0 && h->lr >= 0.0;
 }
 
-template <int Q, bool VEC>
-static void launch_bwd_adamw(const AdamBatch& b, cudaStream_t s) {
+template <int Q, bool VEC, int CAP>
+static void launch_bwd_adamw_cap(const AdamBatchT<CAP>& b, cudaStream_t s) {
     static int cache[64] = {0};
-    auto k = bwd_adamw_units_kernel<Q, VEC>;
+    auto k = bwd_adamw_units_kernel<Q, VEC, CAP>;
     const int64_t ctas = persistent_ctas(k, cache);
     const unsigned grid = static_cast<unsigned>(b.b.total_units < ctas ? b.b.total_units : ctas);
     k<<<grid, kThreads, 0, s>>>(b);
     pqc::count_launch();
+}
+
+template <int Q, bool VEC>
+static void launch_bwd_adamw(const AdamBatch& b, cudaStream_t s) {
+    if (b.b.n > kSmallBatch) return launch_bwd_adamw_cap<Q, VEC, kMaxBatch>(b, s);
+    // the small parameter block, as in the forward and backward
+    static thread_local AdamBatchT<kSmallBatch> sb;
+    sb.b.n = b.b.n;
+    sb.b.pad_ = 0;
+    sb.b.total_units = b.b.total_units;
+    for (int i = 0; i < b.b.n; ++i) sb.b.m[i] = b.b.m[i];
+    sb.kw = b.kw;
+    sb.ka = b.ka;
+    sb.coef = b.coef;
+    launch_bwd_adamw_cap<Q, VEC, kSmallBatch>(sb, s);
 }
 
 static pq_status_t bwd_adamw_impl(int q, int32_t n, const pq_adamw_matrix_t* mats,
