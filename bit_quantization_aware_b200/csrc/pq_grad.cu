@@ -488,6 +488,11 @@ static pq_status_t check_tensor(const pq_tensor_t& t, bool scale) {
     if (scale && t.out) {
         if (t.out_dtype != t.dtype && t.out_dtype != PQ_FP32) return PQ_ERR_INVALID_ARG;
         if (reinterpret_cast<uintptr_t>(t.out) % dtype_bytes(t.out_dtype)) return PQ_ERR_MISALIGNED;
+        // in place, or apart: units are scaled in any order
+        const uintptr_t d = reinterpret_cast<uintptr_t>(t.data), o = reinterpret_cast<uintptr_t>(t.out);
+        const uintptr_t dn = static_cast<uintptr_t>(t.numel) * dtype_bytes(t.dtype);
+        const uintptr_t on = static_cast<uintptr_t>(t.numel) * dtype_bytes(t.out_dtype);
+        if (o < d + dn && d < o + on && !(o == d && t.out_dtype == t.dtype)) return PQ_ERR_INVALID_ARG;
     }
     return PQ_OK;
 }

@@ -514,7 +514,7 @@ def tensor_array(tensors, outs=None):
         raise ValueError("outs must have one entry for each tensor")
     arr = (PQTensor * len(tensors))()
     arr.device_index = _one_device(*tensors, *outs)
-    written = set()
+    spans = []  # (begin, end, written) of every range of memory
     for d, t, o in zip(arr, tensors, outs):
         if t.dtype not in DTYPES:
             raise ValueError(f"gradients must be bf16, fp16 or fp32, not {t.dtype}")
@@ -522,10 +522,21 @@ def tensor_array(tensors, outs=None):
             raise ValueError("an out has its tensor's size and its type or fp32")
         d.data, d.numel, d.dtype = _ptr(t), t.numel(), DTYPES[t.dtype]
         d.out, d.out_dtype = _ptr(o), DTYPES[o.dtype] if o is not None else 0
-        dst = d.out or d.data
-        if t.numel() and dst in written:
-            raise ValueError("two entries would write the same tensor")
-        written.add(dst)
+        size = t.numel() * t.element_size()
+        if not size:
+            continue
+        in_place = o is None or (d.out == d.data and o.dtype == t.dtype)
+        spans.append((d.data, d.data + size, in_place))
+        if not in_place:
+            spans.append((d.out, d.out + o.numel() * o.element_size(), True))
+    spans.sort()
+    end = written_end = 0  # of the ranges before, and of those that are written
+    for begin, stop, written in spans:
+        if begin < (end if written else written_end):
+            raise ValueError("two entries would write the same tensor, or one what another reads")
+        end = max(end, stop)
+        if written:
+            written_end = max(written_end, stop)
     return arr
 
 

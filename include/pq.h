@@ -273,7 +273,8 @@ typedef enum {
 /* One gradient tensor (device pointers; `numel` consecutive elements). A
  * scaling call writes data[i] * coef, rounded once to the output's type, to
  * `out`, or back to `data` when out is NULL. out_dtype is dtype or PQ_FP32;
- * out overlaps no other tensor's data or out. Pointers are aligned to their
+ * out is data itself (same type) or overlaps neither it nor another tensor's
+ * data or out. Pointers are aligned to their
  * element; 32-byte aligned tensors take the vector path, others an element
  * path with the same results. Norm calls ignore out and out_dtype. */
 typedef struct {

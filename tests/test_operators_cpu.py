@@ -255,3 +255,26 @@ def test_reference_rounding_is_e4m3():
     assert torch.equal(R.e4m3(v), v.float().to(torch.float8_e4m3fn).double())
     assert torch.equal(R.e4m3(torch.tensor([1e6, -500.0, 448.1], dtype=torch.float64)),
                        torch.tensor([448.0, -448.0, 448.0], dtype=torch.float64))
+
+
+def test_overlapping_gradients_are_refused(pq):
+    """Units are scaled in any order, so no entry may write memory that another
+    one, or its own input, uses."""
+    t = lambda at, n=8, dtype=torch.float32: FakeCuda(torch.zeros(n, dtype=dtype), at)
+    A, B = 0x10000, 0x10020  # B is right behind eight fp32 values at A
+    ok = [([t(A), t(B)], None), ([t(A)], [t(A)]), ([t(A), t(A)], [t(B), t(0x20000)]),
+          ([t(A, 8, torch.bfloat16)], [t(A + 16)]), ([t(A, 0), t(A)], None)]
+    for tensors, outs in ok:
+        assert len(pq.tensor_array(tensors, outs)) == len(tensors)
+    bad = [([t(A), t(A + 16)], None),                  # views that share half
+           ([t(A, 64), t(B), t(0x20000)], None),       # one inside another
+           ([t(A), t(B)], [t(B), t(0x20000)]),         # an out over another's data
+           ([t(A), t(B)], [t(0x20000), t(0x20010)]),   # outs that share half
+           ([t(A)], [t(A + 4)]),                       # its own data, shifted
+           ([t(A, 8, torch.bfloat16)], [t(A)])]        # fp32 over its own bf16 data
+    for tensors, outs in bad:
+        with pytest.raises(ValueError, match="two entries"):
+            pq.tensor_array(tensors, outs)
+    for dtype, at in ((pq.PQ_FP32, A + 4), (pq.PQ_BF16, A), (pq.PQ_BF16, A + 12), (pq.PQ_FP32, A - 28)):
+        arr = (pq.PQTensor * 1)(pq.PQTensor(A, 8, at, dtype, pq.PQ_FP32))
+        assert pq.lib().pq_grad_scale(1, arr, FAKE, None) == pq.PQ_ERR_INVALID_ARG, (dtype, at)
