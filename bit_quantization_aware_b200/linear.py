@@ -57,6 +57,11 @@ class Fp8Linear:
         if t.dim() != 2 or tuple(t.shape) != (rows, cols):
             raise ValueError(f"Fp8Linear: {name} must be [{rows}, {cols}], got {list(t.shape)}")
 
+    @staticmethod
+    def _out(rows, cols, like, stream):
+        with pq._allocate_on(stream):
+            return torch.empty((rows, cols), dtype=torch.bfloat16, device=like.device)
+
     def forward(self, x, wq, y_out=None, stream=None):
         """y = x Wq^T (bf16 [tokens, out_features], or ``y_out``'s type) from x
         [tokens, in_features] and wq [out_features, in_features]."""
@@ -67,7 +72,7 @@ class Fp8Linear:
         self._check(wq, self.n, self.k, "wq")
         w, wt = self._w.quant(wq, stream)
         xr, xt = self._x.quant(x, stream)
-        y = y_out if y_out is not None else torch.empty((m, self.n), dtype=torch.bfloat16, device=x.device)
+        y = y_out if y_out is not None else self._out(m, self.n, x, stream)
         pq.pq_fp8_gemm(*xr, *w, pq.PQ_BLOCK_TILE, y, stream)
         self._saved = (m, wt, xt)
         return y
@@ -80,8 +85,8 @@ class Fp8Linear:
         m, wt, xt = self._saved
         self._check(dy, m, self.n, "dy")
         dyr, dyt = self._dy.quant(dy, stream)
-        dx = dx_out if dx_out is not None else torch.empty((m, self.k), dtype=torch.bfloat16, device=dy.device)
-        dw = dw_out if dw_out is not None else torch.empty((self.n, self.k), dtype=torch.bfloat16, device=dy.device)
+        dx = dx_out if dx_out is not None else self._out(m, self.k, dy, stream)
+        dw = dw_out if dw_out is not None else self._out(self.n, self.k, dy, stream)
         pq.pq_fp8_gemm(*dyr, *wt, pq.PQ_BLOCK_TILE, dx, stream)
         pq.pq_fp8_gemm(*dyt, *xt, pq.PQ_BLOCK_ROW, dw, stream)
         return dx, dw

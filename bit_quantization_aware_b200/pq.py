@@ -12,6 +12,7 @@ status.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -230,6 +231,17 @@ def _stream(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _allocate_on(stream):
+    """Context whose allocations belong to ``stream`` (None: the current one):
+    memory of the current stream's pool may still be in use there when another
+    stream writes it, and is given out again while that one still runs."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _check(fn, status):
@@ -605,8 +617,9 @@ def clip_grad_norm(tensors, max_norm, stream=None):
     if not tensors:
         raise ValueError("clip_grad_norm needs at least one tensor")
     dev = tensors[0].device
-    norm = torch.empty(1, dtype=torch.float32, device=dev)
-    ws = torch.empty(pq_grad_norm_workspace_bytes(len(tensors)), dtype=torch.uint8, device=dev)
+    with _allocate_on(stream):
+        norm = torch.empty(1, dtype=torch.float32, device=dev)
+        ws = torch.empty(pq_grad_norm_workspace_bytes(len(tensors)), dtype=torch.uint8, device=dev)
     pq_grad_clip(tensor_array(tensors), max_norm, norm, None, ws, stream)
     return norm
 
@@ -688,12 +701,13 @@ def fp8_quant(x, block=PQ_BLOCK_ROW, transposed=False, stream=None):
     None unless ``transposed``."""
     rows, cols = x.shape
     dev = x.device
-    q = fp8_empty(rows, cols, dev)
-    s = torch.empty(fp8_scale_shape(block, rows, cols), dtype=torch.float32, device=dev)
     qt = st = None
-    if transposed:
-        qt = fp8_empty(cols, rows, dev)
-        st = torch.empty(fp8_scale_shape(block, cols, rows), dtype=torch.float32, device=dev)
+    with _allocate_on(stream):
+        q = fp8_empty(rows, cols, dev)
+        s = torch.empty(fp8_scale_shape(block, rows, cols), dtype=torch.float32, device=dev)
+        if transposed:
+            qt = fp8_empty(cols, rows, dev)
+            st = torch.empty(fp8_scale_shape(block, cols, rows), dtype=torch.float32, device=dev)
     pq_fp8_quant(block, x, q, s, qt, st, stream)
     return q, s, qt, st
 
@@ -717,7 +731,8 @@ def pq_fp8_gemm(a, a_scale, b, b_scale, b_block, y_out, stream=None):
 
 def fp8_gemm(a, a_scale, b, b_scale, b_block=PQ_BLOCK_TILE, out_dtype=torch.bfloat16, stream=None):
     """Allocate the output and run pq_fp8_gemm."""
-    y = torch.empty((a.shape[0], b.shape[0]), dtype=out_dtype, device=a.device)
+    with _allocate_on(stream):
+        y = torch.empty((a.shape[0], b.shape[0]), dtype=out_dtype, device=a.device)
     pq_fp8_gemm(a, a_scale, b, b_scale, b_block, y, stream)
     return y
 

@@ -292,3 +292,33 @@ def test_linear_gradients_against_differences(pq):
     loss = lambda y: float((y * dy.double()).sum())
     assert loss(run(x + ux, w)) - loss(y0) == float((dx.cpu().double() * ux.double()).sum())
     assert loss(run(x, w + uw)) - loss(y0) == float((dw.cpu().double() * uw.double()).sum())
+
+
+@pytest.mark.parametrize("as_int", [False, True])
+def test_outputs_belong_to_the_stream_that_writes_them(pq, as_int):
+    """Memory that the current stream's pool holds free may still be in use
+    there: a call on another stream takes none of it."""
+    from bit_quantization_aware_b200.linear import Fp8Linear
+    m, n, k = 700, 640, 512
+    x, w = (draw(r, k, r, torch.bfloat16).to(DEV) for r in (m, n))
+    dy = draw(m, n, 1, torch.bfloat16).to(DEV)
+    layer = Fp8Linear(n, k, m, device=DEV)
+    want = [pq.fp8_gemm(*pq.fp8_quant(x)[:2], *pq.fp8_quant(w, 2)[:2])]
+    want += [layer.forward(x, w), *layer.backward(dy)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if as_int else side
+    # every size that the calls allocate, free in the current stream's pool
+    free = [torch.empty(b, dtype=torch.uint8, device=DEV)
+            for b in (m * k, n * k, 4 * 4 * m, 4 * 5 * 4, 2 * m * n, 2 * m * k, 2 * n * k) for _ in range(4)]
+    held = [(t.data_ptr(), t.data_ptr() + t.numel()) for t in free]
+    del free
+    q = pq.fp8_quant(x, stream=stream)
+    b = pq.fp8_quant(w, 2, stream=stream)
+    y = pq.fp8_gemm(*q[:2], *b[:2], stream=stream)
+    got = [y, layer.forward(x, w, stream=stream), *layer.backward(dy, stream=stream)]
+    side.synchronize()
+    for t in (*q[:2], *b[:2], *got):
+        assert not any(lo <= t.data_ptr() < hi for lo, hi in held)
+    for a, e in zip(got, want):
+        assert torch.equal(a, e)

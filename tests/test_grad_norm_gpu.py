@@ -480,3 +480,23 @@ def test_quant_step_norm_and_clip(pq):
     for t, k in zip([t for b in st.bufs for t in (b.dw, b.dalpha)], grads):
         # the two norms may round differently: factors within an fp32 step
         assert torch.allclose(t, k * c, rtol=2.0 ** -22, atol=0)
+
+
+@pytest.mark.parametrize("as_int", [False, True])
+def test_clipping_workspace_belongs_to_the_stream(pq, monkeypatch, as_int):
+    """clip_grad_norm returns while its kernels run: the workspace that it
+    gives back must not go to the current stream's next allocation."""
+    ts = [torch.randn(n, generator=torch.Generator().manual_seed(n)).to("cuda") for n in (5, 4096, 100001)]
+    want = float(torch.cat([t.double() for t in ts]).norm())
+    torch.cuda.synchronize()
+    seen = []
+    call = pq.pq_grad_clip
+    monkeypatch.setattr(pq, "pq_grad_clip", lambda *a: (seen.append((a[2], a[4].data_ptr(), a[4].numel())), call(*a)))
+    side = torch.cuda.Stream()
+    norm = pq.clip_grad_norm(ts, 1.0, side.cuda_stream if as_int else side)
+    _, at, size = seen[0]
+    taken = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert all(t.data_ptr() != at for t in taken)
+    side.synchronize()
+    # the norm: fp64 sums rounded once to fp32
+    assert abs(float(norm) - want) <= want * (torch.finfo(torch.float32).eps / 2 + 1e-12)
