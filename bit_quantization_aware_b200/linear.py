@@ -70,6 +70,7 @@ class Fp8Linear:
             raise ValueError(f"Fp8Linear: 1 to {self.max_tokens} tokens, got {m}")
         self._check(x, m, self.k, "x")
         self._check(wq, self.n, self.k, "wq")
+        self._saved = None  # its codes are overwritten from here on
         w, wt = self._w.quant(wq, stream)
         xr, xt = self._x.quant(x, stream)
         y = y_out if y_out is not None else self._out(m, self.n, x, stream)

@@ -278,3 +278,29 @@ def test_overlapping_gradients_are_refused(pq):
     for dtype, at in ((pq.PQ_FP32, A + 4), (pq.PQ_BF16, A), (pq.PQ_BF16, A + 12), (pq.PQ_FP32, A - 28)):
         arr = (pq.PQTensor * 1)(pq.PQTensor(A, 8, at, dtype, pq.PQ_FP32))
         assert pq.lib().pq_grad_scale(1, arr, FAKE, None) == pq.PQ_ERR_INVALID_ARG, (dtype, at)
+
+
+def test_linear_forgets_a_forward_that_another_broke_into(pq, monkeypatch):
+    """A forward that fails halfway has overwritten the weights' codes of the
+    one before: backward refuses instead of mixing the two."""
+    from bit_quantization_aware_b200.linear import Fp8Linear
+    monkeypatch.setattr(pq, "pq_fp8_quant", lambda *a: None)
+    monkeypatch.setattr(pq, "pq_fp8_gemm", lambda *a: None)
+    layer = Fp8Linear(6, 4, 5, device="cpu")
+    x, w, dy = torch.zeros(2, 4), torch.zeros(6, 4), torch.zeros(2, 6)
+    layer.forward(x, w)
+    with pytest.raises(ValueError):  # refused before anything is written: the last forward stands
+        layer.forward(torch.zeros(2, 3), w)
+    layer.backward(dy)
+
+    def refuse(*a):
+        raise ValueError("y_out")
+
+    monkeypatch.setattr(pq, "pq_fp8_gemm", refuse)
+    with pytest.raises(ValueError, match="y_out"):
+        layer.forward(x, w)
+    monkeypatch.setattr(pq, "pq_fp8_gemm", lambda *a: None)
+    with pytest.raises(ValueError, match="forward first"):
+        layer.backward(dy)
+    layer.forward(x, w)
+    layer.backward(dy)
