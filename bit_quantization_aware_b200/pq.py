@@ -356,6 +356,7 @@ def pq_fakequant_bwd_adamw(q, mats, hp_w, hp_alpha, stream=None, coef=None):
     """Backward fused with one AdamW step over a ``pq_adamw_matrix_t[]``;
     ``coef`` (fp32 [1], from ``pq_grad_norm``) clips the gradients."""
     if coef is not None:
+        _one_device(coef)
         _check("pq_fakequant_bwd_adamw_clip", lib().pq_fakequant_bwd_adamw_clip(
             q, len(mats), mats, ctypes.byref(hp_w), ctypes.byref(hp_alpha), _f32_1(coef, "coef"),
             _stream(stream)))
@@ -388,6 +389,7 @@ def pq_reduce_bwd_adamw(q, g_sources, grad_mult, shards, hp_w, hp_alpha, stream=
     ``coef`` (fp32 [1], from ``pq_clip_coef``) clips the gradients."""
     srcs = (ctypes.c_void_p * len(g_sources))(*[_ptr(g) for g in g_sources])
     if coef is not None:
+        _one_device(coef)
         _check("pq_reduce_bwd_adamw_clip", lib().pq_reduce_bwd_adamw_clip(
             q, len(g_sources), srcs, ctypes.c_float(grad_mult), len(shards), shards,
             ctypes.byref(hp_w), ctypes.byref(hp_alpha), _f32_1(coef, "coef"), _stream(stream)))
@@ -575,6 +577,7 @@ def pq_reduce_grad_norm(q, g_sources, grad_mult, shards, max_norm, norm_out, coe
                         sumsq_out=None, stream=None):
     """``pq_grad_norm`` of row shards (see ``shard_array``), each gradient the
     replicas' sum as in ``pq_reduce_bwd_adamw``."""
+    _one_device(workspace, norm_out, coef_out, sumsq_out)  # the gradients may be peers'
     srcs = (ctypes.c_void_p * len(g_sources))(*[_ptr(g) for g in g_sources])
     ws, ws_bytes = _workspace(workspace)
     _check("pq_reduce_grad_norm", lib().pq_reduce_grad_norm(

@@ -304,3 +304,25 @@ def test_linear_forgets_a_forward_that_another_broke_into(pq, monkeypatch):
         layer.backward(dy)
     layer.forward(x, w)
     layer.backward(dy)
+
+
+def test_clipping_factors_of_another_device_are_refused(pq, monkeypatch):
+    class On(FakeCuda):
+        def __init__(self, dev, *shape, dtype=torch.float32):
+            super().__init__(torch.zeros(*shape, dtype=dtype))
+            self.dev = dev
+
+        def get_device(self):
+            return self.dev
+
+    monkeypatch.setattr(pq, "_current_device", lambda: 0)
+    hp = pq.adamw(1, 1e-3)
+    n0 = pq.pq_launch_count()
+    with pytest.raises(ValueError, match="current device is cuda:0"):
+        pq.pq_fakequant_bwd_adamw(pq.PQ_SEQ2, pq.adamw_matrix_array([]), hp, hp, coef=On(1, 1))
+    with pytest.raises(ValueError, match="current device is cuda:0"):
+        pq.pq_reduce_bwd_adamw(pq.PQ_SEQ2, [0x10000], 1.0, pq.shard_array([]), hp, hp, coef=On(1, 1))
+    with pytest.raises(ValueError, match="different devices"):
+        pq.pq_reduce_grad_norm(pq.PQ_SEQ2, [0x10000], 1.0, pq.shard_array([]), 1.0, On(0, 1), None,
+                               On(1, 64, dtype=torch.uint8))
+    assert pq.pq_launch_count() == n0
