@@ -1040,9 +1040,9 @@ static pq_status_t launch(Params& p, const uint8_t* a, int64_t lda, const uint8_
     if (!enc || !encode(enc, &p.ta, kByte, 1, a, p.m, k, lda, a_rows) ||
         !encode(enc, &p.tb, kByte, 1, b, p.n, k, ldb, L::kBRows))
         return PQ_ERR_CUDA;
-    // TMA stores want 16-byte aligned rows
+    // TMA stores want 16-byte aligned rows, less than 2^40 bytes apart
     const int size = bytes_of(p.dtype);
-    p.tma_out = SPLIT == 1 && pq::aligned(p.y, 16) && p.ldy * size % 16 == 0;
+    p.tma_out = SPLIT == 1 && pq::aligned(p.y, 16) && p.ldy < (int64_t{1} << 40) / size && p.ldy * size % 16 == 0;
     if (p.tma_out && !encode(enc, &p.ty, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
                              size, p.y, p.m, p.n, p.ldy, 32))
         return PQ_ERR_CUDA;

@@ -308,7 +308,8 @@ class ShardedQuantStep:
         gradients: this rank's shards add their squares, ``gather`` (fp64 [1]
         of this rank -> fp64 [world] of all, ordered with the stream like the
         barrier; not needed for one rank) collects the ranks' sums, and every
-        rank adds them in the same order, so all clip alike."""
+        rank adds them in the same order, so all clip alike. Both are this
+        object's buffers, which its next call overwrites."""
         if gather is None and self.world > 1:
             raise ValueError("clip_coef needs a gather over the ranks' sums")
         sources, mult, shards = self._reduce_args(grad_mult)

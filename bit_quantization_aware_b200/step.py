@@ -145,14 +145,16 @@ class QuantStep:
     def grad_norm(self, max_norm, stream=None):
         """(norm, clipping factor), fp32 [1] each, of the quantizer gradients
         of every matrix, formed from w, alpha and g without dW: the factor is
-        what ``pq_fakequant_bwd_adamw`` takes as ``coef``."""
+        what ``pq_fakequant_bwd_adamw`` takes as ``coef``. Both are this
+        object's buffers, which its next call overwrites."""
         ws, norm, coef = self._norm_buffers(len(self.bufs))
         pq.pq_grad_norm(max_norm, norm, coef, ws, q=self.q, mats=self._bwd_descs, stream=stream)
         return norm, coef
 
     def clip_grads(self, max_norm, stream=None):
         """Clips the dW and d(alpha) that ``bwd_all`` wrote by their global
-        norm, in place; returns the norm before it (fp32 [1])."""
+        norm, in place; returns the norm before it (fp32 [1],
+        this object's buffer, which its next call overwrites)."""
         if self._clip_descs is None:
             self._clip_descs = pq.tensor_array([t for b in self.bufs if b.m.rows
                                                 for t in ((b.dw, b.dalpha) if b.m.cols else (b.dalpha,))])

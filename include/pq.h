@@ -298,7 +298,8 @@ typedef struct {
  * squares is kept and the same call gives the same bits. An Inf gradient
  * gives norm = Inf and coef = 0 (Inf * 0 = NaN where it is scaled); a NaN
  * makes both NaN. No gradients give norm 0 and coef 1.
- *   max_norm     >= 0; infinity gives coef 1 for every finite norm
+ *   max_norm     >= 0; infinity gives coef 1 for every finite norm (and NaN for
+ *                an infinite one)
  *   sumsq_out    nullable double[1]: the sum of squares, e.g. one rank's
  *                part of a sharded step (see pq_clip_coef)
  *   norm_out     nullable float[1];   coef_out  nullable float[1]; at least
@@ -404,7 +405,9 @@ PQ_API pq_status_t pq_fp8_quant(pq_block_t block, pq_dtype_t dtype, int64_t rows
  *   dx [tokens, in]  = gemm(dy rows,          W^T tiles)
  *   dW [out, in]     = gemm(dy^T rows,        x^T rows)
  *   a, lda, a_scale  codes [m, k], row r at byte r * lda, PQ_BLOCK_ROW scales
- *   b, ldb, b_scale  codes [n, k], b_block scales
+ *   b, ldb, b_scale  codes [n, k], b_block scales. With tiles sa * sb is
+ *                    formed first (rounded once), so it is meant to be a
+ *                    normal fp32 number; with rows sb is applied first
  *   y, ldy           [m, n] of y_dtype, row r at element r * ldy, overwritten
  * Codes are 16-byte aligned and lda, ldb multiples of 16 (TMA), else
  * PQ_ERR_MISALIGNED; any m, n, k >= 0 (k == 0 writes zeros); Y of any
@@ -601,7 +604,7 @@ PQ_API pq_status_t pq_wq_gemm_noalloc(pq_quant_t q, int64_t m, int64_t n, int64_
                                       const float* alpha, uint16_t* y_bf16, void* stream);
 
 /* Device status of the library's bounded waits (the weight-only matmul
- * waits on mbarriers; every wait has an iteration cap): PQ_OK if none gave
+ * and the e4m3 product wait on mbarriers; every wait has an iteration cap): PQ_OK if none gave
  * up since the last call, PQ_ERR_TIMEOUT if one did (the status is then
  * cleared), PQ_ERR_CUDA if the status could not be read. A kernel whose wait
  * gave up stops all its roles, lets its copies and MMAs in flight finish,

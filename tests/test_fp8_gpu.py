@@ -322,3 +322,15 @@ def test_outputs_belong_to_the_stream_that_writes_them(pq, as_int):
         assert not any(lo <= t.data_ptr() < hi for lo, hi in held)
     for a, e in zip(got, want):
         assert torch.equal(a, e)
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_one_row_of_any_pitch(pq, out):
+    """One row has no pitch to speak of: a number that no TMA map takes is
+    no reason to refuse it."""
+    n, k = 4000, 128  # one K block: not split
+    a, b = pq.fp8_quant(draw(1, k, 1).to(DEV))[:2], pq.fp8_quant(draw(n, k, 2).to(DEV), 2)[:2]
+    want = pq.fp8_gemm(*a, *b, out_dtype=out)
+    y = torch.empty(n, dtype=out, device=DEV).as_strided((1, n), (1 << 41, 1))
+    pq.pq_fp8_gemm(*a, *b, pq.PQ_BLOCK_TILE, y)
+    assert torch.equal(y[0], want[0])
