@@ -166,13 +166,14 @@ __device__ __forceinline__ int locate(const BatchT<D, CAP>& b, int64_t u) {
 }
 
 // ----------------------------------------------------------------- tensors
-struct TensorDesc {
+struct TensorDesc {  // 32 bytes: 256 of them go with a launch
     const void* g;
     void* out;
-    int64_t n;
+    int64_t n_vec;    // 2 n + 1 where vector accesses are aligned (32 bytes), else 2 n
     int64_t unit_begin;
-    int32_t vec;      // 32-byte aligned: vector accesses
-    int32_t inplace;
+    __device__ __forceinline__ int64_t n() const { return n_vec >> 1; }
+    __device__ __forceinline__ bool vec() const { return n_vec & 1; }
+    __device__ __forceinline__ bool inplace() const { return out == g; }
 };
 
 template <typename T, int CAP>
@@ -194,9 +195,9 @@ norm_tensors_kernel(const __grid_constant__ NormBatch<T, CAP> P) {
         const TensorDesc& t = P.b.m[mi];
         const int64_t base = (u - t.unit_begin) * kUnit;
         const T* g = static_cast<const T*>(t.g) + base;
-        const int n = static_cast<int>(t.n - base < kUnit ? t.n - base : kUnit);
+        const int n = static_cast<int>(t.n() - base < kUnit ? t.n() - base : kUnit);
         int done = 0;
-        if (t.vec) {
+        if (t.vec()) {
             Vec<T> v[kVecsPerThread];
             done = n / V * V;
 #pragma unroll
@@ -290,13 +291,13 @@ scale_tensors_kernel(const __grid_constant__ ScaleBatch<T, O, CAP> P) {
         const int64_t u = P.b.total_units - 1 - r;
         while (P.b.m[mi].unit_begin > u) --mi;
         const TensorDesc& t = P.b.m[mi];
-        if (t.inplace && c == 1.0f) continue;
+        if (t.inplace() && c == 1.0f) continue;
         const int64_t base = (u - t.unit_begin) * kUnit;
         const T* g = static_cast<const T*>(t.g) + base;
         O* out = static_cast<O*>(t.out) + base;
-        const int n = static_cast<int>(t.n - base < kUnit ? t.n - base : kUnit);
+        const int n = static_cast<int>(t.n() - base < kUnit ? t.n() - base : kUnit);
         int done = 0;
-        if (t.vec) {
+        if (t.vec()) {
             Vec<T> v[kVecsPerThread];
             done = n / V * V;
 #pragma unroll
@@ -594,10 +595,8 @@ static void tensor_batch_add(BatchT<TensorDesc>& b, const pq_tensor_t& t) {
     TensorDesc& d = b.m[b.n++];
     d.g = t.data;
     d.out = t.out ? t.out : t.data;
-    d.n = t.numel;
+    d.n_vec = 2 * t.numel + (aligned(t.data, kVecBytes) && aligned(d.out, kVecBytes));
     d.unit_begin = b.total_units;
-    d.vec = aligned(t.data, kVecBytes) && aligned(d.out, kVecBytes);
-    d.inplace = d.out == t.data;
     const int64_t unit = kUnitBytes / dtype_bytes(t.dtype);
     b.total_units += (t.numel + unit - 1) / unit;
 }
@@ -605,7 +604,11 @@ static void tensor_batch_add(BatchT<TensorDesc>& b, const pq_tensor_t& t) {
 // Partial sums of the tensors, one launch per dtype and 256 tensors.
 static pq_status_t norm_tensors(int32_t n, const pq_tensor_t* ts, Partials& parts, cudaStream_t s) {
     static thread_local BatchT<TensorDesc> b;
+    uint32_t present = 0;
+    for (int32_t i = 0; i < n; ++i)
+        if (ts[i].numel) present |= 1u << ts[i].dtype;
     for (int dtype : {PQ_BF16, PQ_FP16, PQ_FP32}) {
+        if (!(present >> dtype & 1u)) continue;
         b.n = 0;
         b.total_units = 0;
         auto flush = [&]() -> pq_status_t {
@@ -636,9 +639,13 @@ static pq_status_t norm_tensors(int32_t n, const pq_tensor_t* ts, Partials& part
 static pq_status_t scale_tensors(int32_t n, const pq_tensor_t* ts, const float* coef, const NormEnd& end,
                                  bool& scaled, cudaStream_t s) {
     static thread_local BatchT<TensorDesc> b;
+    uint32_t present = 0;  // pairs of dtypes
+    for (int32_t i = 0; i < n; ++i)
+        if (ts[i].numel) present |= 1u << (4 * ts[i].dtype + out_dtype_of(ts[i]));
     for (int cls = 0; cls < 5; ++cls) {
         static constexpr int kIn[5] = {PQ_BF16, PQ_BF16, PQ_FP16, PQ_FP16, PQ_FP32};
         static constexpr int kOut[5] = {PQ_BF16, PQ_FP32, PQ_FP16, PQ_FP32, PQ_FP32};
+        if (!(present >> (4 * kIn[cls] + kOut[cls]) & 1u)) continue;
         b.n = 0;
         b.total_units = 0;
         auto flush = [&]() -> pq_status_t {

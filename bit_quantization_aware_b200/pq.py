@@ -12,7 +12,6 @@ status.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -233,15 +232,17 @@ def _stream(stream):
     return stream.cuda_stream
 
 
-def _allocate_on(stream):
-    """Context whose allocations belong to ``stream`` (None: the current one):
-    memory of the current stream's pool may still be in use there when another
-    stream writes it, and is given out again while that one still runs."""
+def _new(like, shape, dtype, stream):
+    """Uninitialised tensor beside ``like`` that belongs to ``stream`` (None:
+    the current one): memory of the current stream's pool may still be in use
+    there when another stream writes it, and is given out again while that one
+    still runs."""
     if stream is None:
-        return contextlib.nullcontext()
+        return like.new_empty(shape, dtype=dtype)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-    return torch.cuda.stream(stream)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _check(fn, status):
@@ -488,14 +489,16 @@ def pq_wq_gemm_noalloc(q, x, packed, alpha, y_out, stream=None):
 def _one_device(*tensors):
     """The tensors' device index; raises unless they share one and it is the
     current device, whose stream and context the kernels run in."""
-    found = {t if isinstance(t, int) else t.get_device() for t in tensors if t is not None}
-    found.discard(-1)
-    if not found:
-        return -1
-    if len(found) > 1:
-        raise ValueError("tensors on different devices: " + ", ".join(f"cuda:{d}" for d in sorted(found)))
-    dev = found.pop()
-    if dev != _current_device():
+    dev = -1
+    for t in tensors:
+        if t is None:
+            continue
+        d = t if isinstance(t, int) else t.get_device()
+        if d != dev and d >= 0:
+            if dev >= 0:
+                raise ValueError(f"tensors on different devices: cuda:{dev}, cuda:{d}")
+            dev = d
+    if dev >= 0 and dev != _current_device():
         raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{_current_device()}")
     return dev
 
@@ -619,10 +622,8 @@ def clip_grad_norm(tensors, max_norm, stream=None):
     tensors = list(tensors)
     if not tensors:
         raise ValueError("clip_grad_norm needs at least one tensor")
-    dev = tensors[0].device
-    with _allocate_on(stream):
-        norm = torch.empty(1, dtype=torch.float32, device=dev)
-        ws = torch.empty(pq_grad_norm_workspace_bytes(len(tensors)), dtype=torch.uint8, device=dev)
+    norm = _new(tensors[0], (1,), torch.float32, stream)
+    ws = _new(tensors[0], (pq_grad_norm_workspace_bytes(len(tensors)),), torch.uint8, stream)
     pq_grad_clip(tensor_array(tensors), max_norm, norm, None, ws, stream)
     return norm
 
@@ -699,18 +700,19 @@ def fp8_empty(rows, cols, device):
     return q if pitch == cols else q[:, :cols]
 
 
+def _codes_and_scales(like, block, rows, cols, stream):
+    pitch = (cols + 15) // 16 * 16
+    q = _new(like, (rows, pitch), torch.float8_e4m3fn, stream)
+    return (q if pitch == cols else q[:, :cols],
+            _new(like, fp8_scale_shape(block, rows, cols), torch.float32, stream))
+
+
 def fp8_quant(x, block=PQ_BLOCK_ROW, transposed=False, stream=None):
     """Allocate outputs and quantize x; returns (q, s, qt, st), the last two
     None unless ``transposed``."""
     rows, cols = x.shape
-    dev = x.device
-    qt = st = None
-    with _allocate_on(stream):
-        q = fp8_empty(rows, cols, dev)
-        s = torch.empty(fp8_scale_shape(block, rows, cols), dtype=torch.float32, device=dev)
-        if transposed:
-            qt = fp8_empty(cols, rows, dev)
-            st = torch.empty(fp8_scale_shape(block, cols, rows), dtype=torch.float32, device=dev)
+    q, s = _codes_and_scales(x, block, rows, cols, stream)
+    qt, st = _codes_and_scales(x, block, cols, rows, stream) if transposed else (None, None)
     pq_fp8_quant(block, x, q, s, qt, st, stream)
     return q, s, qt, st
 
@@ -734,8 +736,7 @@ def pq_fp8_gemm(a, a_scale, b, b_scale, b_block, y_out, stream=None):
 
 def fp8_gemm(a, a_scale, b, b_scale, b_block=PQ_BLOCK_TILE, out_dtype=torch.bfloat16, stream=None):
     """Allocate the output and run pq_fp8_gemm."""
-    with _allocate_on(stream):
-        y = torch.empty((a.shape[0], b.shape[0]), dtype=out_dtype, device=a.device)
+    y = _new(a, (a.shape[0], b.shape[0]), out_dtype, stream)
     pq_fp8_gemm(a, a_scale, b, b_scale, b_block, y, stream)
     return y
 
