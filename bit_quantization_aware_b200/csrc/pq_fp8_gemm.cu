@@ -79,14 +79,16 @@ struct Layout {
     static constexpr int kBBytes = kParts * kBRows * kBlock;
     static constexpr uint32_t kTmemCols = kBufs * NT;
     static constexpr int kCtas = NT == 64 ? 2 : 1;        // resident on an SM
-    // full, empty, pair [stages]; dfull, dempty [halves x buffers]; sfull,
-    // sempty [scale slots]; drain [halves]; TMEM base, abort
-    static constexpr int kNumBars = 3 * kMaxStages + 2 * kParts * kBufs + 2 * kScaleSlots + 2;
-    static constexpr int kMiscOff = 8 * kNumBars;
+    // full, empty [stages]; dfull, dempty [halves x buffers]; sfull, sempty
+    // [scale slots]; drain [halves]; TMEM base, abort, and a pair's words: the
+    // K blocks that this CTA loaded, its place in the ring of stages (slot and
+    // phase), the other CTA's K blocks and abort
+    static constexpr int kNumBars = 2 * kMaxStages + 2 * kParts * kBufs + 2 * kScaleSlots + 2;
+    static constexpr int kMiscOff = 8 * kNumBars, kPairOff = kMiscOff + 8;
     static constexpr int kScaleOff = 1024;
     static constexpr int kOutOff = kScaleOff + (BROW ? kScaleSlots * NT * 4 : 0);  // 4 KB a promote warp
     static constexpr int kRingOff = kOutOff + (SPLIT == 1 ? kPromoteWarps * 4096 : 0);
-    static_assert(kMiscOff + 8 <= kScaleOff && kOutOff % 1024 == 0, "shared memory layout");
+    static_assert(kPairOff + 20 <= kScaleOff && kOutOff % 1024 == 0, "shared memory layout");
     // exchange of a split tile: [from rank][row][column of the slice, padded]
     static constexpr int kSlice = NT / SPLIT, kPitch = kSlice + 4;
     static_assert(SPLIT == 1 || (!PAIR && kSlice % 8 == 0), "slices of whole vectors");
@@ -115,6 +117,13 @@ struct StageRing {
             idx = 0;
             phase ^= 1u;
         }
+    }
+    __device__ __forceinline__ void prev() {
+        if (idx == 0) {
+            idx = n;
+            phase ^= 1u;
+        }
+        --idx;
     }
 };
 
@@ -164,10 +173,11 @@ __device__ __forceinline__ void mbar_arrive_if(uint32_t mbar, bool yes) {
         : "memory");
 }
 
-// Arrival on a barrier of the cluster, without release (a release took above
-// 1000 cycles): the threads that arrive so have written no memory. They have
-// read tensor memory (tcgen05.wait::ld is over) or seen copies land, which the
-// tensor cores read where they are.
+// Arrival on a barrier of the cluster, without release (with one, the pairs
+// took twice their time): the threads that arrive so have written no memory.
+// They have read tensor memory: tcgen05.wait::ld and the fence before the
+// arrival, and the fence behind the wait, order those reads before the MMAs
+// that follow, as PTX has it for a relaxed barrier between them.
 __device__ __forceinline__ void mbar_arrive_cluster_if(uint32_t addr, bool yes) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t"
@@ -176,15 +186,44 @@ __device__ __forceinline__ void mbar_arrive_cluster_if(uint32_t addr, bool yes) 
         : "memory");
 }
 
-// Whether the phase is over, for the whole warp alike. REMOTE: arrivals from
-// the other CTA, which publish no memory (see mbar_arrive_cluster).
-template <bool REMOTE>
+// A pair's loads: each CTA brings its operands into its own shared memory and
+// both arrive, and count their bytes, on the issuing CTA's barrier (an address
+// of the cluster's shared memory), so the wait of the thread that issues the
+// MMAs covers both CTAs' copies. Copies may land before the arrival that
+// announces their bytes: the phase lasts until both CTAs have arrived.
+__device__ __forceinline__ void mbar_expect_tx_cluster(uint32_t mbar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(mbar), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t mbar, int32_t x,
+                                                 int32_t y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(mbar), "r"(x), "r"(y)
+        : "memory");
+}
+
+// Whom a wait hears from: this CTA; both CTAs' copies (a pair's operands); the
+// other CTA's arrivals, which publish no memory (see mbar_arrive_cluster_if).
+enum Heard { kCta, kCopies, kRemote };
+
+// Whether the phase is over, for the whole warp alike.
+template <int HEARD>
 __device__ __forceinline__ bool mbar_try_warp(uint32_t mbar, uint32_t parity) {
     uint32_t done;
-    if constexpr (REMOTE)
+    if constexpr (HEARD == kRemote)
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
             "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(done)
+            : "r"(mbar), "r"(parity)
+            : "memory");
+    else if constexpr (HEARD == kCopies)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}\n"
             : "=r"(done)
             : "r"(mbar), "r"(parity)
@@ -196,35 +235,25 @@ __device__ __forceinline__ bool mbar_try_warp(uint32_t mbar, uint32_t parity) {
 
 // The same asked ahead: the answer takes some 100 to 200 cycles, in which the
 // warp does other work.
-template <bool REMOTE>
 __device__ __forceinline__ uint32_t mbar_test(uint32_t mbar, uint32_t parity) {
     uint32_t done;
-    if constexpr (REMOTE)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}\n"
-            : "=r"(done)
-            : "r"(mbar), "r"(parity)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}\n"
-            : "=r"(done)
-            : "r"(mbar), "r"(parity)
-            : "memory");
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(mbar), "r"(parity)
+        : "memory");
     return done;
 }
 
 // Bounded wait of a whole warp, which stays converged and uniform. A round
 // trip between two warps over two such waits measured 175 cycles, one lane's
 // wait with a shuffle of its result 425.
-template <bool REMOTE>
+template <int HEARD = kCta>
 __device__ __forceinline__ bool uniform_wait(uint32_t mbar, uint32_t parity, volatile int* abort) {
     for (uint32_t i = 0; i < kMaxSpins; ++i) {
-        if (mbar_try_warp<REMOTE>(mbar, parity)) return true;
+        if (mbar_try_warp<HEARD>(mbar, parity)) return true;
         if ((i & 63u) == 63u && __any_sync(0xFFFFFFFFu, *abort)) return false;
     }
     *abort = 1;
@@ -324,6 +353,10 @@ __device__ __forceinline__ void st_cluster(uint32_t a, float x, float y, float z
 }
 __device__ __forceinline__ void st_cluster(uint32_t a, float x, float y) {
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(x), "f"(y) : "memory");
+}
+__device__ __forceinline__ void st_cluster(uint32_t a, uint32_t x, uint32_t y) {
+    asm volatile("st.shared::cluster.b32 [%0], %1;\n\tst.shared::cluster.b32 [%0 + 4], %2;" ::"r"(a), "r"(x), "r"(y)
+                 : "memory");
 }
 __device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
     uint32_t a;
@@ -470,22 +503,22 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t{1023});
     const uint32_t sbase = smem_u32(smem);
-    const uint32_t b_full = sbase, b_empty = b_full + 8u * kMaxStages, b_pair = b_empty + 8u * kMaxStages;
+    const uint32_t b_full = sbase, b_empty = b_full + 8u * kMaxStages;
     constexpr uint32_t kD = 8u * L::kParts * L::kBufs;
-    const uint32_t b_dfull = b_pair + 8u * kMaxStages, b_dempty = b_dfull + kD;
+    const uint32_t b_dfull = b_empty + 8u * kMaxStages, b_dempty = b_dfull + kD;
     const uint32_t b_sfull = b_dempty + kD, b_sempty = b_sfull + 8u * kScaleSlots;
     const uint32_t b_drain = b_sempty + 8u * kScaleSlots;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
     volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
+    volatile uint32_t* pair_words = reinterpret_cast<volatile uint32_t*>(smem + L::kPairOff);
     const float* scales = reinterpret_cast<const float*>(smem + L::kScaleOff);
     const uint32_t a_ring = sbase + L::kRingOff, b_ring = a_ring + p.stages * p.a_bytes;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
         for (int s = 0; s < p.stages; ++s) {
-            mbar_init(b_full + 8u * s, 1);
+            mbar_init(b_full + 8u * s, L::kParts);  // PAIR: both CTAs' producers
             mbar_init(b_empty + 8u * s, L::kParts);
-            mbar_init(b_pair + 8u * s, 1);
         }
         for (int b = 0; b < L::kParts * L::kBufs; ++b) {
             mbar_init(b_dfull + 8u * b, 1);
@@ -545,7 +578,8 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
             // ------------------------------------------------------ producer
             if (lane == 0) {
                 StageRing r(p.stages);
-                int issued = 0;
+                uint32_t loaded = 0;  // K blocks
+                const uint32_t full = PAIR ? map_to_rank(b_full, 0) : b_full;  // the issuer's
                 bool ok = true;
                 for (int t = first; ok && t < tiles; t += step) {
                     int tm, tn;
@@ -557,25 +591,34 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
                             ok = false;
                             break;
                         }
-                        const uint32_t bar = b_full + 8u * r.idx;
-                        mbar_expect_tx(bar, static_cast<uint32_t>(p.a_bytes) + L::kBBytes);
-                        tma_load_2d(a_ring + r.idx * p.a_bytes, &p.ta, bar, kb * kBlock, ra);
+                        const uint32_t bar = full + 8u * r.idx, bytes = static_cast<uint32_t>(p.a_bytes) + L::kBBytes;
+                        const uint32_t a = a_ring + r.idx * p.a_bytes, b = b_ring + r.idx * L::kBBytes;
+                        if constexpr (PAIR) {
+                            mbar_expect_tx_cluster(bar, bytes);
+                            tma_load_2d_pair(a, &p.ta, bar, kb * kBlock, ra);
 #pragma unroll
-                        for (int h = 0; h < L::kParts; ++h)
-                            tma_load_2d(b_ring + r.idx * L::kBBytes + h * L::kBRows * kBlock, &p.tb, bar, kb * kBlock,
-                                        rb + h * L::kCols);
+                            for (int h = 0; h < L::kParts; ++h)
+                                tma_load_2d_pair(b + h * L::kBRows * kBlock, &p.tb, bar, kb * kBlock, rb + h * L::kCols);
+                        } else {
+                            mbar_expect_tx(bar, bytes);
+                            tma_load_2d(a, &p.ta, bar, kb * kBlock, ra);
+                            tma_load_2d(b, &p.tb, bar, kb * kBlock, rb);
+                        }
                         r.next();
-                        if (issued < p.stages) ++issued;
+                        ++loaded;
                     }
                 }
-                // loads in flight land before the CTA may exit
-                for (; issued > 0; --issued) {
-                    if (r.idx == 0) {
-                        r.idx = r.n;
-                        r.phase ^= 1u;
+                // loads in flight land before the CTA may exit (a pair's: see
+                // the end of the kernel)
+                if constexpr (PAIR) {
+                    pair_words[0] = loaded;
+                    pair_words[1] = r.idx;
+                    pair_words[2] = r.phase;
+                } else {
+                    for (uint32_t i = min(loaded, r.n); i > 0; --i) {
+                        r.prev();
+                        mbar_drain(b_full + 8u * r.idx, r.phase);
                     }
-                    --r.idx;
-                    mbar_drain(b_full + 8u * r.idx, r.phase);
                 }
             }
             __syncwarp();
@@ -605,20 +648,17 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
                         const uint32_t acc = tmem + (d.idx * L::kParts + h) * L::kCols;
                         const uint32_t free_bar = b_empty + 8u * r.idx, full_bar = dfull + 8u * d.idx;
                         if (!(kAhead && __any_sync(0xFFFFFFFFu, ready)) &&
-                            (!uniform_wait<false>(b_full + 8u * r.idx, r.phase, abort) ||
-                             (PAIR && !uniform_wait<true>(b_pair + 8u * r.idx, r.phase, abort)) ||
-                             !uniform_wait<PAIR>(dempty + 8u * d.idx, d.phase ^ 1u, abort))) {
+                            (!uniform_wait<PAIR ? kCopies : kCta>(b_full + 8u * r.idx, r.phase, abort) ||
+                             !uniform_wait<PAIR ? kRemote : kCta>(dempty + 8u * d.idx, d.phase ^ 1u, abort))) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
                         r.next();
                         d.next();
-                        if constexpr (kAhead) {
-                            ready = mbar_test<false>(b_full + 8u * r.idx, r.phase) &
-                                    mbar_test<PAIR>(dempty + 8u * d.idx, d.phase ^ 1u);
-                            if constexpr (PAIR) ready &= mbar_test<true>(b_pair + 8u * r.idx, r.phase);
-                        }
+                        if constexpr (kAhead)
+                            ready = mbar_test(b_full + 8u * r.idx, r.phase) &
+                                    mbar_test(dempty + 8u * d.idx, d.phase ^ 1u);
                         if (one) {
 #pragma unroll
                             for (int k = 0; k < kBlock / 32; ++k)
@@ -635,21 +675,8 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
                     mbar_drain(b_drain + 8u * h, 0);
                 }
             } else {
-                // ------- the pair's other CTA: its operands are here, too
-                const uint32_t pair0 = map_to_rank(b_pair, 0);
-                const bool one = elect_one();
-                StageRing r(p.stages);
-                bool ok = true;
-                for (int t = first; ok && t < tiles; t += step)
-                    for (int kb = k0; kb < k1; ++kb) {
-                        if (!uniform_wait<false>(b_full + 8u * r.idx, r.phase, abort)) {
-                            ok = false;
-                            break;
-                        }
-                        mbar_arrive_cluster_if(pair0 + 8u * r.idx, one);
-                        r.next();
-                    }
-                if (one)  // the issuers' last arrivals here
+                // ------- the pair's other CTA: the issuers' last arrivals here
+                if (elect_one())
                     for (int h = 0; h < L::kParts; ++h) mbar_drain(b_drain + 8u * h, 0);
             }
             __syncwarp();
@@ -728,7 +755,7 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
             if (k0 >= k1) return true;
             fetch(k0);
             uint32_t v[2][W];
-            if (!uniform_wait<false>(dfull + 8u * d.idx, d.phase, abort)) return false;
+            if (!uniform_wait(dfull + 8u * d.idx, d.phase, abort)) return false;
             tc_fence_after();
             tmem_ld(buffer(), v[0]);
             for (int kb = k0; kb < k1; ++kb) {
@@ -751,7 +778,7 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
                 for (int c = 0; c + W < C; c += W) {
                     tmem_wait(v[c / W % 2]);
                     tmem_ld(src + c + W, v[(c / W + 1) % 2]);
-                    if (c == (C > 3 * W ? C - 3 * W : 0)) ready = mbar_test<false>(dfull + 8u * d.idx, d.phase);
+                    if (c == (C > 3 * W ? C - 3 * W : 0)) ready = mbar_test(dfull + 8u * d.idx, d.phase);
                     add(c);
                 }
                 tmem_wait(v[(C / W - 1) % 2]);
@@ -764,7 +791,7 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
                         continue;
                     }
                     add(C - W);
-                    if (!uniform_wait<false>(dfull + 8u * d.idx, d.phase, abort)) return false;
+                    if (!uniform_wait(dfull + 8u * d.idx, d.phase, abort)) return false;
                     tc_fence_after();
                     tmem_ld(buffer(), v[0]);
                 } else {
@@ -799,8 +826,8 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
                 for (int i = 0; i < 4; ++i) a[i] = next[i];
                 fetch(kb + 2, next);
                 if (!__any_sync(0xFFFFFFFFu, ready) &&
-                    (!uniform_wait<false>(b_sfull + 8u * sr.idx, sr.phase, abort) ||
-                     !uniform_wait<false>(dfull + 8u * d.idx, d.phase, abort)))
+                    (!uniform_wait(b_sfull + 8u * sr.idx, sr.phase, abort) ||
+                     !uniform_wait(dfull + 8u * d.idx, d.phase, abort)))
                     return false;
                 tc_fence_after();
                 const float* bs = scales + sr.idx * NT + part * C + 2 * (lane % 4);
@@ -822,8 +849,8 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
                         else if (c + 32 < C) tmem_ld_rows(src + c + 32, v[0]);
                         else free_buffer(free_bar);
                         if (g == 1 && c + 64 == C)
-                            ready = mbar_test<false>(b_sfull + 8u * sr.idx, sr.phase) &
-                                    mbar_test<false>(dfull + 8u * d.idx, d.phase);
+                            ready = mbar_test(b_sfull + 8u * sr.idx, sr.phase) &
+                                    mbar_test(dfull + 8u * d.idx, d.phase);
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -916,8 +943,34 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
     tc_fence_before();
     __syncthreads();
     // PAIR: neither CTA frees its memory while the other's MMAs, commits and
-    // arrivals reach it
-    if constexpr (PAIR) cluster_sync();
+    // arrivals reach it, or its own loads are in flight. Where no wait gave up,
+    // the issuers have waited for every load of both.
+    if constexpr (PAIR) {
+        if (tid == 0) st_cluster(map_to_rank(sbase + L::kPairOff + 12, rank ^ 1), pair_words[0], *abort);
+        cluster_sync();
+        if (*abort || pair_words[4]) {
+            if (rank == 0 && tid == 0) {
+                // One producer may have loaded up to the ring's length of K
+                // blocks more than the other: the missing arrivals come from
+                // here, and every load has landed when the phases are over.
+                StageRing r(p.stages);
+                r.idx = pair_words[1];
+                r.phase = pair_words[2];
+                const uint32_t n0 = pair_words[0], n1 = pair_words[3];
+                for (uint32_t i = n0; i < n1; ++i, r.next()) mbar_arrive(b_full + 8u * r.idx);
+                StageRing q = r;
+                for (uint32_t i = n1; i < n0; ++i) {
+                    q.prev();
+                    mbar_arrive(b_full + 8u * q.idx);
+                }
+                for (uint32_t i = min(max(n0, n1), r.n); i > 0; --i) {
+                    r.prev();
+                    mbar_drain(b_full + 8u * r.idx, r.phase);
+                }
+            }
+            cluster_sync();
+        }
+    }
     if (warp == 2) {
         if constexpr (PAIR)
             asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::kTmemCols)
