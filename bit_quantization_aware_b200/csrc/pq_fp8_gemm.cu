@@ -208,7 +208,8 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
 // other CTA's arrivals, which publish no memory (see mbar_arrive_cluster_if).
 enum Heard { kCta, kCopies, kRemote };
 
-// Whether the phase is over, for the whole warp alike.
+// Whether the phase is over, for the whole warp alike: once every lane has
+// seen it, since a vote orders no memory and each lane acquires for itself.
 template <int HEARD>
 __device__ __forceinline__ bool mbar_try_warp(uint32_t mbar, uint32_t parity) {
     uint32_t done;
@@ -230,7 +231,7 @@ __device__ __forceinline__ bool mbar_try_warp(uint32_t mbar, uint32_t parity) {
             : "memory");
     else
         done = mbar_try(mbar, parity);
-    return __any_sync(0xFFFFFFFFu, done);
+    return __all_sync(0xFFFFFFFFu, done);
 }
 
 // The same asked ahead: the answer takes some 100 to 200 cycles, in which the
@@ -647,7 +648,7 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
                         const uint64_t b = sw128_desc(b_ring + r.idx * L::kBBytes + h * L::kBRows * kBlock);
                         const uint32_t acc = tmem + (d.idx * L::kParts + h) * L::kCols;
                         const uint32_t free_bar = b_empty + 8u * r.idx, full_bar = dfull + 8u * d.idx;
-                        if (!(kAhead && __any_sync(0xFFFFFFFFu, ready)) &&
+                        if (!(kAhead && __all_sync(0xFFFFFFFFu, ready)) &&
                             (!uniform_wait<PAIR ? kCopies : kCta>(b_full + 8u * r.idx, r.phase, abort) ||
                              !uniform_wait<PAIR ? kRemote : kCta>(dempty + 8u * d.idx, d.phase ^ 1u, abort))) {
                             ok = false;
@@ -784,7 +785,7 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
                 tmem_wait(v[(C / W - 1) % 2]);
                 free_buffer(free_bar);  // all read: the issuer may write the buffer again
                 if (kb + 1 < k1) {
-                    if (__any_sync(0xFFFFFFFFu, ready)) {
+                    if (__all_sync(0xFFFFFFFFu, ready)) {
                         tc_fence_after();
                         tmem_ld(buffer(), v[0]);
                         add(C - W);
@@ -825,7 +826,7 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) a[i] = next[i];
                 fetch(kb + 2, next);
-                if (!__any_sync(0xFFFFFFFFu, ready) &&
+                if (!__all_sync(0xFFFFFFFFu, ready) &&
                     (!uniform_wait(b_sfull + 8u * sr.idx, sr.phase, abort) ||
                      !uniform_wait(dfull + 8u * d.idx, d.phase, abort)))
                     return false;
