@@ -219,7 +219,15 @@ class ShardedQuantStep:
         self.m_a = torch.zeros(nr, dtype=torch.float32, device=dev)
         self.v_a = torch.zeros(nr, dtype=torch.float32, device=dev)
         self.dalpha = torch.zeros(nr, dtype=torch.float32, device=dev)
-        self._clip = None  # buffers of clip_coef, from its first call
+        # clip_coef's workspace, sum of squares, norm and factor: made here,
+        # where the caller can order them with whatever stream the calls take
+        # (a stand-in may lack the norm)
+        self._clip = None
+        if hasattr(lib, "pq_grad_norm_workspace_bytes"):
+            self._clip = (torch.empty(lib.pq_grad_norm_workspace_bytes(0, len(self.mats)),
+                                      dtype=torch.uint8, device=dev),
+                          torch.empty(1, dtype=torch.float64, device=dev),
+                          torch.empty(1, device=dev), torch.empty(1, device=dev))
 
     # ---------------------------------------------------------- views
     def my_rows(self, i):
@@ -313,12 +321,6 @@ class ShardedQuantStep:
         if gather is None and self.world > 1:
             raise ValueError("clip_coef needs a gather over the ranks' sums")
         sources, mult, shards = self._reduce_args(grad_mult)
-        if self._clip is None:  # workspace, sum of squares, norm, factor
-            dev = self.device
-            self._clip = (torch.empty(self.lib.pq_grad_norm_workspace_bytes(0, len(self.mats)),
-                                      dtype=torch.uint8, device=dev),
-                          torch.zeros(1, dtype=torch.float64, device=dev),
-                          torch.zeros(1, device=dev), torch.zeros(1, device=dev))
         ws, sumsq, norm, coef = self._clip
         self.lib.pq_reduce_grad_norm(self.q, sources, mult, shards, max_norm, None, None, ws,
                                      sumsq_out=sumsq, stream=stream)

@@ -89,7 +89,15 @@ class QuantStep:
                  dw=b.dw, dalpha=b.dalpha, grad_scale=b.grad_scale)
             for b in self.bufs])
 
-        self._norm, self._clip_descs = {}, None
+        # workspace, norm and factor of grad_norm and of clip_grads: made here,
+        # where the caller can order them with whatever stream the calls take
+        def norm_buffers(tensors, matrices):
+            ws = torch.empty(pq.pq_grad_norm_workspace_bytes(tensors, matrices), dtype=torch.uint8, device=dev)
+            return ws, torch.empty(1, device=dev), torch.empty(1, device=dev)
+
+        self._norm = norm_buffers(0, len(self.bufs))
+        self._clip = norm_buffers(2 * len(self.bufs), 0)
+        self._clip_descs = None
 
     @property
     def weights(self) -> int:
@@ -133,21 +141,12 @@ class QuantStep:
             pq.pq_fakequant_bwd(self.q, b.w, b.alpha, b.g, b.dw, b.dalpha,
                                 b.grad_scale, stream)
 
-    def _norm_buffers(self, n):
-        """Workspace for n entries, norm and factor (kept: a captured call
-        goes on using them)."""
-        if n not in self._norm:
-            dev = self.device
-            self._norm[n] = (torch.empty(pq.pq_grad_norm_workspace_bytes(n, n), dtype=torch.uint8, device=dev),
-                             torch.zeros(1, device=dev), torch.zeros(1, device=dev))
-        return self._norm[n]
-
     def grad_norm(self, max_norm, stream=None):
         """(norm, clipping factor), fp32 [1] each, of the quantizer gradients
         of every matrix, formed from w, alpha and g without dW: the factor is
         what ``pq_fakequant_bwd_adamw`` takes as ``coef``. Both are this
         object's buffers, which its next call overwrites."""
-        ws, norm, coef = self._norm_buffers(len(self.bufs))
+        ws, norm, coef = self._norm
         pq.pq_grad_norm(max_norm, norm, coef, ws, q=self.q, mats=self._bwd_descs, stream=stream)
         return norm, coef
 
@@ -158,7 +157,7 @@ class QuantStep:
         if self._clip_descs is None:
             self._clip_descs = pq.tensor_array([t for b in self.bufs if b.m.rows
                                                 for t in ((b.dw, b.dalpha) if b.m.cols else (b.dalpha,))])
-        ws, norm, coef = self._norm_buffers(len(self._clip_descs))
+        ws, norm, coef = self._clip
         pq.pq_grad_clip(self._clip_descs, max_norm, norm, coef, ws, stream)
         return norm
 
