@@ -89,6 +89,11 @@ class QuantStep:
                  dw=b.dw, dalpha=b.dalpha, grad_scale=b.grad_scale)
             for b in self.bufs])
 
+        # what grad_norm reads, without dW and d(alpha): a norm writes neither
+        self._norm_descs = pq.matrix_array([
+            dict(rows=b.m.rows, cols=b.m.cols, w=b.w, alpha=b.alpha, g=b.g,
+                 grad_scale=b.grad_scale) for b in self.bufs])
+
         # workspace, norm and factor of grad_norm and of clip_grads: made here,
         # where the caller can order them with whatever stream the calls take
         def norm_buffers(tensors, matrices):
@@ -143,11 +148,12 @@ class QuantStep:
 
     def grad_norm(self, max_norm, stream=None):
         """(norm, clipping factor), fp32 [1] each, of the quantizer gradients
-        of every matrix, formed from w, alpha and g without dW: the factor is
-        what ``pq_fakequant_bwd_adamw`` takes as ``coef``. Both are this
-        object's buffers, which its next call overwrites."""
+        of every matrix, formed from w, alpha and g: the factor is what
+        ``pq_fakequant_bwd_adamw`` takes as ``coef``. The matrices' dW and
+        d(alpha) stay as they are. Both results are this object's buffers,
+        which its next call overwrites."""
         ws, norm, coef = self._norm
-        pq.pq_grad_norm(max_norm, norm, coef, ws, q=self.q, mats=self._bwd_descs, stream=stream)
+        pq.pq_grad_norm(max_norm, norm, coef, ws, q=self.q, mats=self._norm_descs, stream=stream)
         return norm, coef
 
     def clip_grads(self, max_norm, stream=None):

@@ -59,3 +59,11 @@ def test_sharded_step_makes_its_norm_buffers_when_it_is_made(monkeypatch):
         norm, coef = st.clip_coef(1.0, stream=77)
     assert float(norm) == 2.0
 
+
+
+def test_quant_step_norm_writes_no_gradient(pq):
+    st = step(pq)
+    st.grad_norm(1.0)
+    mats = pq.calls[0][1]["mats"]
+    assert [m["g"].data_ptr() for m in mats] == [b.g.data_ptr() for b in st.bufs]
+    assert all(m.get("dalpha") is None and m.get("dw") is None for m in mats)

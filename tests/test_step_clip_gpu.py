@@ -68,3 +68,17 @@ def test_first_sharded_norm_on_another_stream(pq):  # noqa: F811
     assert (float(norm), float(coef)) == early
     assert early[0] == pytest.approx(want, rel=RTOL)
     assert early[1] == pytest.approx(coef_of(want, 0.25 * want), rel=RTOL)
+
+
+def test_norm_after_clipping_leaves_the_clipped_gradients(pq):  # noqa: F811
+    from bit_quantization_aware_b200.step import QuantStep
+    st = QuantStep(MATS, pq.PQ_SEQ2, device=DEV)
+    st.generate(seed=3)
+    st.run()
+    first = float(st.grad_norm(1.0)[0])
+    st.clip_grads(0.25 * first)
+    clipped = [t.clone() for b in st.bufs for t in (b.dw, b.dalpha)]
+    again, _ = st.grad_norm(1.0)  # for a log, say: that of the unclipped gradient
+    assert float(again) == first
+    for t, k in zip([t for b in st.bufs for t in (b.dw, b.dalpha)], clipped):
+        assert torch.equal(t, k)
