@@ -160,6 +160,8 @@ class QuantStep:
         """Clips the dW and d(alpha) that ``bwd_all`` wrote by their global
         norm, in place; returns the norm before it (fp32 [1],
         this object's buffer, which its next call overwrites)."""
+        if self.dw_all is None:
+            raise ValueError("clip_grads needs the dW of bwd_all (alloc_outputs=True)")
         if self._clip_descs is None:
             self._clip_descs = pq.tensor_array([t for b in self.bufs if b.m.rows
                                                 for t in ((b.dw, b.dalpha) if b.m.cols else (b.dalpha,))])

@@ -67,3 +67,11 @@ def test_quant_step_norm_writes_no_gradient(pq):
     mats = pq.calls[0][1]["mats"]
     assert [m["g"].data_ptr() for m in mats] == [b.g.data_ptr() for b in st.bufs]
     assert all(m.get("dalpha") is None and m.get("dw") is None for m in mats)
+
+
+def test_clipping_without_outputs_is_refused(pq):
+    st = step(pq, alloc_outputs=False)
+    with pytest.raises(ValueError, match="alloc_outputs"):
+        st.clip_grads(1.0)
+    st.grad_norm(1.0)  # which needs none
+    assert len(pq.calls) == 1
