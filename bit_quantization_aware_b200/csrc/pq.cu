@@ -1243,6 +1243,7 @@ pq_status_t pq_fakequant_bwd_adamw_clip(pq_quant_t q, int32_t n, const pq_adamw_
                                         const pq_adamw_t* hp_w, const pq_adamw_t* hp_alpha,
                                         const float* coef, void* stream) {
     if (!coef) return PQ_ERR_INVALID_ARG;
+    if (!aligned(coef, 4)) return PQ_ERR_MISALIGNED;
     return bwd_adamw_impl(q, n, mats, hp_w, hp_alpha, coef, static_cast<cudaStream_t>(stream));
 }
 
@@ -1258,6 +1259,7 @@ pq_status_t pq_reduce_bwd_adamw_clip(pq_quant_t q, int32_t n_src, const uint16_t
                                      const pq_adamw_t* hp_w, const pq_adamw_t* hp_alpha,
                                      const float* coef, void* stream) {
     if (!coef) return PQ_ERR_INVALID_ARG;
+    if (!aligned(coef, 4)) return PQ_ERR_MISALIGNED;
     return reduce_bwd_adamw_impl(q, n_src, g_sources, grad_mult, n, shards, hp_w, hp_alpha, coef,
                                  static_cast<cudaStream_t>(stream));
 }

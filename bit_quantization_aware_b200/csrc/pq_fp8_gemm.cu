@@ -1173,6 +1173,7 @@ extern "C" pq_status_t pq_fp8_gemm(int64_t m, int64_t n, int64_t k, const uint8_
     if (n == 1) ldb = (k + 15) / 16 * 16;
     if (m > (int64_t{1} << 30) || n > (int64_t{1} << 30) || k > (int64_t{1} << 30)) return PQ_ERR_UNSUPPORTED;
     if (!pq::aligned(a, 16) || !pq::aligned(b, 16) || lda % 16 || ldb % 16) return PQ_ERR_MISALIGNED;
+    if (!pq::aligned(a_scale, 4) || !pq::aligned(b_scale, 4)) return PQ_ERR_MISALIGNED;
     Params p = {};
     p.sa = a_scale;
     p.sb = b_scale;

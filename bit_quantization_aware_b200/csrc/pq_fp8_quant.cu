@@ -408,6 +408,7 @@ extern "C" pq_status_t pq_fp8_quant(pq_block_t block, pq_dtype_t dtype, int64_t 
     if (!x || (!q_out && !qt_out)) return PQ_ERR_INVALID_ARG;
     if (ldx < cols || (q_out && ldq < cols) || (qt_out && ldqt < rows)) return PQ_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(x) % (dtype == PQ_FP32 ? 4 : 2)) return PQ_ERR_MISALIGNED;
+    if (!pq::aligned(s_out, 4) || !pq::aligned(st_out, 4)) return PQ_ERR_MISALIGNED;
     pqf::QuantParams P = {x, rows, cols, ldx, q_out, ldq, s_out, qt_out, ldqt, st_out,
                           (rows + 127) / 128, (cols + 127) / 128};
     // one CTA a tile (or 16 rows x 4 blocks): at most 2^31 - 1 of them

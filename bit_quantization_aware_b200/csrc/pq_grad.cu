@@ -763,6 +763,8 @@ static pq_status_t check_mats(int q, int32_t n, const pq_matrix_t* mats) {
         const pq_matrix_t& m = mats[i];
         if (m.rows < 0 || m.cols < 0) return PQ_ERR_INVALID_ARG;
         if (m.rows > 0 && m.cols > 0 && (!m.w || !m.alpha || !m.g_bf16)) return PQ_ERR_INVALID_ARG;
+        if (!aligned(m.w, 4) || !aligned(m.alpha, 4) || !aligned(m.g_bf16, 2) || !aligned(m.dalpha_out, 4))
+            return PQ_ERR_MISALIGNED;
     }
     return PQ_OK;
 }
@@ -774,6 +776,11 @@ static pq_status_t check_tensors(int32_t n, const pq_tensor_t* ts, bool scale) {
         if (st != PQ_OK) return st;
     }
     return PQ_OK;
+}
+
+// The scalars that a norm writes, each nullable.
+static bool scalars_aligned(const double* sumsq, const float* norm, const float* coef) {
+    return aligned(sumsq, 8) && aligned(norm, 4) && aligned(coef, 4);
 }
 
 static NormEnd norm_end(const Partials& parts, double max_norm, double* sumsq, float* norm, float* coef) {
@@ -804,6 +811,7 @@ pq_status_t pq_grad_norm(int32_t n, const pq_tensor_t* tensors, pq_quant_t q, in
     if (st == PQ_OK) st = check_mats(q, n_mats, mats);
     if (st != PQ_OK) return st;
     if (!max_norm_ok(max_norm) || (!sumsq_out && !norm_out && !coef_out)) return PQ_ERR_INVALID_ARG;
+    if (!scalars_aligned(sumsq_out, norm_out, coef_out)) return PQ_ERR_MISALIGNED;
     Partials parts;
     st = take_workspace(workspace, workspace_bytes_, workspace_bytes(n, n_mats), parts);
     if (st != PQ_OK) return st;
@@ -845,11 +853,13 @@ pq_status_t pq_reduce_grad_norm(pq_quant_t q, int32_t n_src, const uint16_t* con
     if (code_bits_of(q) == 0 || n < 0 || (n > 0 && !shards)) return PQ_ERR_INVALID_ARG;
     if (n_src < 1 || n_src > kMaxSources || !g_sources) return PQ_ERR_INVALID_ARG;
     if (!max_norm_ok(max_norm) || (!sumsq_out && !norm_out && !coef_out)) return PQ_ERR_INVALID_ARG;
+    if (!scalars_aligned(sumsq_out, norm_out, coef_out)) return PQ_ERR_MISALIGNED;
     static thread_local GradBatch<kMaxBatch> b;
     bool src_aligned = true;
     for (int k = 0; k < kMaxSources; ++k) {
         b.src[k] = k < n_src ? g_sources[k] : nullptr;
         if (k < n_src && !g_sources[k]) return PQ_ERR_INVALID_ARG;
+        if (!aligned(b.src[k], 2)) return PQ_ERR_MISALIGNED;
         src_aligned = src_aligned && aligned(b.src[k], 16);
     }
     b.n_src = n_src;
@@ -858,6 +868,7 @@ pq_status_t pq_reduce_grad_norm(pq_quant_t q, int32_t n_src, const uint16_t* con
         const pq_shard_t& m = shards[i];
         if (m.rows < 0 || m.cols < 0 || m.g_offset < 0) return PQ_ERR_INVALID_ARG;
         if (m.rows > 0 && m.cols > 0 && (!m.alpha || !m.w)) return PQ_ERR_INVALID_ARG;
+        if (!aligned(m.w, 4) || !aligned(m.alpha, 4) || !aligned(m.dalpha_out, 4)) return PQ_ERR_MISALIGNED;
     }
     Partials parts;
     pq_status_t st = take_workspace(workspace, workspace_bytes_, workspace_bytes(0, n), parts);
@@ -889,6 +900,7 @@ pq_status_t pq_clip_coef(int32_t count, const double* sumsq, double max_norm, fl
                          float* coef_out, void* stream) {
     if (count < 0 || (count > 0 && !sumsq) || !max_norm_ok(max_norm) || (!norm_out && !coef_out))
         return PQ_ERR_INVALID_ARG;
+    if (!scalars_aligned(sumsq, norm_out, coef_out)) return PQ_ERR_MISALIGNED;
     Partials parts = {const_cast<double*>(sumsq), count, count};
     return cuda_status(launch_after(norm_end_kernel, 1, norm_end(parts, max_norm, nullptr, norm_out, coef_out),
                                     static_cast<cudaStream_t>(stream)));
@@ -898,6 +910,7 @@ pq_status_t pq_grad_scale(int32_t n, const pq_tensor_t* tensors, const float* co
     const pq_status_t st = check_tensors(n, tensors, true);
     if (st != PQ_OK) return st;
     if (!coef) return PQ_ERR_INVALID_ARG;
+    if (!aligned(coef, 4)) return PQ_ERR_MISALIGNED;
     bool scaled = false;
     return scale_tensors(n, tensors, coef, NormEnd{}, scaled, static_cast<cudaStream_t>(stream));
 }
@@ -907,6 +920,7 @@ pq_status_t pq_grad_clip(int32_t n, const pq_tensor_t* tensors, double max_norm,
     pq_status_t st = check_tensors(n, tensors, true);
     if (st != PQ_OK) return st;
     if (!max_norm_ok(max_norm) || !norm_out) return PQ_ERR_INVALID_ARG;
+    if (!scalars_aligned(nullptr, norm_out, coef_out)) return PQ_ERR_MISALIGNED;
     Partials parts;
     st = take_workspace(workspace, workspace_bytes_, workspace_bytes(n, 0), parts);
     if (st != PQ_OK) return st;

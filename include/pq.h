@@ -87,7 +87,9 @@ typedef enum {
     PQ_OK = 0,
     PQ_ERR_INVALID_ARG = 1, /* null pointer, negative size, bad enum, bad pack shape */
     PQ_ERR_UNSUPPORTED = 2, /* valid request the library does not serve */
-    PQ_ERR_MISALIGNED = 3,  /* reserved: misaligned input is served by the element path */
+    PQ_ERR_MISALIGNED = 3,  /* a pointer not aligned to its element (gradient norm, clipping and
+                             * e4m3 calls), or codes that TMA cannot read; the quantizer's calls
+                             * serve input that vectors cannot reach by the element path */
     PQ_ERR_CUDA = 4,        /* a CUDA runtime call or launch failed */
     PQ_ERR_TIMEOUT = 5      /* reserved for bounded device-side waits */
 } pq_status_t;
@@ -300,6 +302,7 @@ typedef struct {
  * makes both NaN. No gradients give norm 0 and coef 1.
  *   max_norm     >= 0; infinity gives coef 1 for every finite norm (and NaN for
  *                an infinite one)
+ *   every pointer is aligned to its element, else PQ_ERR_MISALIGNED
  *   sumsq_out    nullable double[1]: the sum of squares, e.g. one rank's
  *                part of a sharded step (see pq_clip_coef)
  *   norm_out     nullable float[1];   coef_out  nullable float[1]; at least
@@ -376,7 +379,8 @@ typedef enum {
  * mantissa bits, largest value 448): for every block
  *     amax = max(max |x|, 2^-96),  scale = fl(amax / 448),
  *     code = e4m3(fl(x * fl(448 / amax)))   (nearest, ties to even, saturating)
- * The last block of a row or column may be short. A NaN or Inf in a block
+ * The last block of a row or column may be short. x and the scales are aligned
+ * to their elements, else PQ_ERR_MISALIGNED. A NaN or Inf in a block
  * makes its scale NaN or Inf, and the products that read it NaN.
  *   dtype        type of x: PQ_BF16, PQ_FP16 or PQ_FP32
  *   x, ldx       [rows, cols], row r at element r * ldx (ldx >= cols)
@@ -410,8 +414,8 @@ PQ_API pq_status_t pq_fp8_quant(pq_block_t block, pq_dtype_t dtype, int64_t rows
  *                    normal fp32 number; with rows sb is applied first
  *   y, ldy           [m, n] of y_dtype, row r at element r * ldy, overwritten
  * Codes are 16-byte aligned and lda, ldb multiples of 16 (TMA), else
- * PQ_ERR_MISALIGNED; any m, n, k >= 0 (k == 0 writes zeros); Y of any
- * alignment. Nothing is allocated and no workspace is needed. Waits inside
+ * PQ_ERR_MISALIGNED; any m, n, k >= 0 (k == 0 writes zeros); scales and Y of
+ * any alignment that suits their elements. Nothing is allocated and no workspace is needed. Waits inside
  * the kernel are bounded; pq_device_status() reports one that gave up.
  * Traffic: (m + n) k B read, m n elements written; 2 m n k flops. */
 PQ_API pq_status_t pq_fp8_gemm(int64_t m, int64_t n, int64_t k, const uint8_t* a, int64_t lda,
