@@ -763,7 +763,8 @@ static pq_status_t check_mats(int q, int32_t n, const pq_matrix_t* mats) {
         const pq_matrix_t& m = mats[i];
         if (m.rows < 0 || m.cols < 0) return PQ_ERR_INVALID_ARG;
         if (m.rows > 0 && m.cols > 0 && (!m.w || !m.alpha || !m.g_bf16)) return PQ_ERR_INVALID_ARG;
-        if (!aligned(m.w, 4) || !aligned(m.alpha, 4) || !aligned(m.g_bf16, 2) || !aligned(m.dalpha_out, 4))
+        if (m.rows > 0 &&
+            (!aligned(m.w, 4) || !aligned(m.alpha, 4) || !aligned(m.g_bf16, 2) || !aligned(m.dalpha_out, 4)))
             return PQ_ERR_MISALIGNED;
     }
     return PQ_OK;
@@ -868,7 +869,8 @@ pq_status_t pq_reduce_grad_norm(pq_quant_t q, int32_t n_src, const uint16_t* con
         const pq_shard_t& m = shards[i];
         if (m.rows < 0 || m.cols < 0 || m.g_offset < 0) return PQ_ERR_INVALID_ARG;
         if (m.rows > 0 && m.cols > 0 && (!m.alpha || !m.w)) return PQ_ERR_INVALID_ARG;
-        if (!aligned(m.w, 4) || !aligned(m.alpha, 4) || !aligned(m.dalpha_out, 4)) return PQ_ERR_MISALIGNED;
+        if (m.rows > 0 && (!aligned(m.w, 4) || !aligned(m.alpha, 4) || !aligned(m.dalpha_out, 4)))
+            return PQ_ERR_MISALIGNED;
     }
     Partials parts;
     pq_status_t st = take_workspace(workspace, workspace_bytes_, workspace_bytes(0, n), parts);
