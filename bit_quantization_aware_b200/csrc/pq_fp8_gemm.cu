@@ -1032,8 +1032,9 @@ static int64_t clusters_resident() {
 //   4 + waves * (K blocks of a CTA * time of one + 1 + exchange) microseconds
 // among the kernels. The times of a K block fit what they measured, tile
 // scales / row scales: pairs 0.5 / 0.85 (8192 x 14336 x 4096: 449 us;
-// 4096 x 4096 x 8190 by rows: 209), 128 wide 0.28 / 0.6 (512 x 4096 x 4096:
-// 14.0, in pairs 19.6), 64 wide 0.24 / 0.45, or 0.36 / 0.55 where two CTAs
+// 4096 x 4096 x 8190 by rows: 209), 128 wide 0.28 (512 x 4096 x 4096: 14.0, in
+// pairs 19.6; with row scales 0.6, so that 64 wide, of which two share an SM,
+// is always ahead, and there is no such kernel), 64 wide 0.24 / 0.45, or 0.36 / 0.55 where two CTAs
 // share an SM (77 x 14336 x 4096: 17.0, 128 wide 14.7). The exchange of a
 // split grows with the sums that it moves: 1 x 4096 x 4096 took 13.5 us in
 // one piece, 10.6 by 2 and 8.0 by 4; 300 x 700 x 2000 (64 wide) 9.7, 8.0 and 7.9.
@@ -1044,7 +1045,7 @@ struct Plan {
 static Plan plan(int64_t m, int64_t n, int64_t kb, bool brow) {
     const int64_t sms = pq::sm_count();
     const double rows = m < kRows ? static_cast<double>(m) / kRows : 1.0;
-    Plan best = {128, 1, false};
+    Plan best = {64, 1, false};
     double best_us = 1e30;
     auto consider = [&](Plan pl, int64_t tiles, int64_t resident, double us_kb, double exchange) {
         const int64_t waves = (tiles + resident - 1) / resident;
@@ -1057,16 +1058,18 @@ static Plan plan(int64_t m, int64_t n, int64_t kb, bool brow) {
     consider({256, 1, true}, (m + 255) / 256 * ((n + 255) / 256), sms / 2, brow ? 0.85 : 0.5, 0.0);
     const int64_t tm = (m + kRows - 1) / kRows, t128 = tm * ((n + 127) / 128), t64 = tm * ((n + 63) / 64);
     for (int split = 1; split <= 8 && split <= kb; split *= 2) {
-        const int64_t c128 = split == 1   ? sms
-                             : split == 2 ? clusters_resident<128, 2>()
-                             : split == 4 ? clusters_resident<128, 4>()
-                                          : clusters_resident<128, 8>();
         const int64_t c64 = split == 1   ? 2 * sms
                             : split == 2 ? clusters_resident<64, 2>()
                             : split == 4 ? clusters_resident<64, 4>()
                                          : clusters_resident<64, 8>();
         const double moved = split == 1 ? 0.0 : 0.3 + rows * (split == 2 ? 1.2 : split == 4 ? 2.5 : 5.0);
-        consider({128, split, false}, t128, c128, brow ? 0.6 : 0.28, moved);
+        if (!brow) {
+            const int64_t c128 = split == 1   ? sms
+                                 : split == 2 ? clusters_resident<128, 2>()
+                                 : split == 4 ? clusters_resident<128, 4>()
+                                              : clusters_resident<128, 8>();
+            consider({128, split, false}, t128, c128, 0.28, moved);
+        }
         const bool shared = t64 * split > sms;
         consider({64, split, false}, t64, c64, brow ? (shared ? 0.55 : 0.45) : (shared ? 0.36 : 0.24), moved / 2);
     }
@@ -1129,14 +1132,13 @@ static pq_status_t launch(Params& p, const uint8_t* a, int64_t lda, const uint8_
 template <bool BROW, typename... Args>
 static pq_status_t launch_plan(const Plan& pl, Args&&... args) {
     if (pl.pair) return launch<256, BROW, 1, true>(args...);
-    if (pl.nt == 128) {
-        switch (pl.split) {
-            case 1: return launch<128, BROW, 1, false>(args...);
-            case 2: return launch<128, BROW, 2, false>(args...);
-            case 4: return launch<128, BROW, 4, false>(args...);
-            default: return launch<128, BROW, 8, false>(args...);
-        }
-    }
+    if constexpr (!BROW)
+        if (pl.nt == 128) switch (pl.split) {
+                case 1: return launch<128, BROW, 1, false>(args...);
+                case 2: return launch<128, BROW, 2, false>(args...);
+                case 4: return launch<128, BROW, 4, false>(args...);
+                default: return launch<128, BROW, 8, false>(args...);
+            }
     switch (pl.split) {
         case 1: return launch<64, BROW, 1, false>(args...);
         case 2: return launch<64, BROW, 2, false>(args...);
