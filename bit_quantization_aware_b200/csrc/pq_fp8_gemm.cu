@@ -391,8 +391,10 @@ __device__ __forceinline__ void tile_of(const Params& p, int t, int& tm, int& tn
 // A warp's 32 rows x C columns to y by way of its 4 KB of shared memory, 128
 // bytes of each row at a time (the 128B swizzle: 16-byte chunk c of row r at
 // chunk c ^ (r % 8), so the writes are free of bank conflicts), and from there
-// by the TMA engine, which clips what lies beyond y, or, where y does not suit
-// it, row by row. Direct stores of whole sectors of each thread's row took
+// by the TMA engine, or, where y does not suit it, row by row. The engine clips
+// rows beyond y, but columns only to a multiple of 16 bytes: with n = 198 it
+// wrote columns 198 and 199 of a wider matrix, so an end inside 16 bytes goes
+// row by row, too. Direct stores of whole sectors of each thread's row took
 // 5000 cycles a tile, during which no K block left TMEM; element by element
 // (an odd pitch) they made up most of a small product's time.
 template <typename T, int C, bool ROWS>
@@ -433,7 +435,7 @@ __device__ __forceinline__ void store_typed(const Params& p, uint32_t buf, int l
                              : "memory");
             }
         }
-        if (p.tma_out) {
+        if (p.tma_out && (col + c + W <= p.n || p.n % (16 / B) == 0)) {
             fence_async_smem();
             __syncwarp();
             if (lane == 0 && row0 < p.m && col + c < p.n) {
