@@ -34,6 +34,8 @@
 
 #include <stdint.h>
 
+#include <atomic>
+
 #include "pq.h"
 #include "pq_launches.cuh"
 #include "pq_tc.cuh"
@@ -1078,6 +1080,21 @@ static Plan plan(int64_t m, int64_t n, int64_t kb, bool brow) {
     return best;
 }
 
+// What pq_debug_fp8_force asked for: width << 8 | split, 0 for the estimate.
+static std::atomic<int> g_forced{0};
+
+// The kernel of a problem; false where a forced one cannot take it (row scales
+// have none of 128, and a split CTA has at least one K block).
+static bool choose(int64_t m, int64_t n, int64_t kb, bool brow, Plan& pl) {
+    const int forced = g_forced.load(std::memory_order_relaxed);
+    if (!forced) {
+        pl = plan(m, n, kb, brow);
+        return true;
+    }
+    pl = {forced >> 8, forced & 255, forced >> 8 == 256};
+    return !(brow && pl.nt == 128) && pl.split <= kb;
+}
+
 // A set-up launch: the box of A, the stages that fit beside it, the maps.
 template <int NT, bool BROW, int SPLIT, bool PAIR>
 static pq_status_t launch(Params& p, const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, int64_t k,
@@ -1188,7 +1205,28 @@ extern "C" pq_status_t pq_fp8_gemm(int64_t m, int64_t n, int64_t k, const uint8_
     p.kb = static_cast<int32_t>((k + kBlock - 1) / kBlock);
     p.dtype = y_dtype;
     p.quad = pq::aligned(y, 4 * bytes_of(y_dtype)) && ldy % 4 == 0;
-    const Plan pl = plan(m, n, p.kb, b_block == PQ_BLOCK_ROW);
+    Plan pl;
+    if (!choose(m, n, p.kb, b_block == PQ_BLOCK_ROW, pl)) return PQ_ERR_UNSUPPORTED;
     return b_block == PQ_BLOCK_ROW ? launch_plan<true>(pl, p, a, lda, b, ldb, k, s)
                                    : launch_plan<false>(pl, p, a, lda, b, ldb, k, s);
+}
+
+extern "C" pq_status_t pq_debug_fp8_force(int width, int split) {
+    const bool any = width == 0 && split == 0, one = split == 1 && (width == 64 || width == 128 || width == 256);
+    const bool many = (split == 2 || split == 4 || split == 8) && (width == 64 || width == 128);
+    if (!any && !one && !many) return PQ_ERR_INVALID_ARG;
+    pq8::g_forced.store(width << 8 | split, std::memory_order_relaxed);
+    return PQ_OK;
+}
+
+extern "C" pq_status_t pq_debug_fp8_choice(int64_t m, int64_t n, int64_t k, pq_block_t b_block, int* width,
+                                           int* split) {
+    if (m < 1 || n < 1 || k < 1 || (b_block != PQ_BLOCK_ROW && b_block != PQ_BLOCK_TILE) || !width || !split)
+        return PQ_ERR_INVALID_ARG;
+    pq8::Plan pl;
+    if (!pq8::choose(m, n, (k + pq8::kBlock - 1) / pq8::kBlock, b_block == PQ_BLOCK_ROW, pl))
+        return PQ_ERR_UNSUPPORTED;
+    *width = pl.nt;
+    *split = pl.split;
+    return PQ_OK;
 }

@@ -161,6 +161,10 @@ def _declare(L):
     L.pq_ipc_close.restype = i32
     L.pq_debug_abort_waits.argtypes = [i32]
     L.pq_debug_abort_waits.restype = i32
+    L.pq_debug_fp8_force.argtypes = [i32, i32]
+    L.pq_debug_fp8_force.restype = i32
+    L.pq_debug_fp8_choice.argtypes = [i64, i64, i64, i32, ctypes.POINTER(i32), ctypes.POINTER(i32)]
+    L.pq_debug_fp8_choice.restype = i32
     L.pq_dequant_codes_batch.argtypes = [i32, i32, ctypes.POINTER(PQMatrix), p]
     L.pq_dequant_codes_batch.restype = i32
     L.pq_dequant_codes.argtypes = [i32, i64, i64, p, p, p, p]
@@ -779,6 +783,20 @@ def pq_launch_count() -> int:
 def pq_debug_abort_waits(on: bool) -> None:
     """Test switch: later matmul launches give up their waits at once."""
     _check("pq_debug_abort_waits", lib().pq_debug_abort_waits(1 if on else 0))
+
+
+def pq_debug_fp8_force(width: int, split: int) -> None:
+    """Test switch: later pq_fp8_gemm calls take the kernel with tiles of
+    ``width`` columns and K split over ``split`` CTAs; (0, 0): their own."""
+    _check("pq_debug_fp8_force", lib().pq_debug_fp8_force(width, split))
+
+
+def pq_debug_fp8_choice(m, n, k, b_block):
+    """(width, split) of the kernel that such a product takes."""
+    width, split = ctypes.c_int(), ctypes.c_int()
+    _check("pq_debug_fp8_choice", lib().pq_debug_fp8_choice(
+        m, n, k, b_block, ctypes.byref(width), ctypes.byref(split)))
+    return width.value, split.value
 
 
 def wq_gemm(q, x, packed, alpha, stream=None):

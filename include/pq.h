@@ -623,6 +623,18 @@ PQ_API int pq_device_status(void);
  * outputs of those launches are undefined. Off (0) by default. */
 PQ_API pq_status_t pq_debug_abort_waits(int on);
 
+/* Test switches for the e4m3 product's kernels. pq_debug_fp8_force makes every
+ * later pq_fp8_gemm of the process take the kernel with tiles of `width`
+ * columns (64, 128, or 256: two CTAs a tile) and each tile's K blocks split
+ * over `split` CTAs (1; 2, 4 or 8 for 64 and 128), in place of the one that
+ * the sizes choose; (0, 0) gives the choice back. A product that a forced
+ * kernel cannot take (128 with row scales of B, fewer K blocks than CTAs) is
+ * answered PQ_ERR_UNSUPPORTED. pq_debug_fp8_choice tells which kernel a
+ * product takes on the current device; nothing is launched. */
+PQ_API pq_status_t pq_debug_fp8_force(int width, int split);
+PQ_API pq_status_t pq_debug_fp8_choice(int64_t m, int64_t n, int64_t k, pq_block_t b_block,
+                                       int* width, int* split);
+
 /* Storage width in bits of one packed code: 2 (binary, ternary, SEQ2,
  * SEQ2_B, LSQ2) or 4 (LSQ3, LSQ4); 0 for an unknown quantizer. */
 PQ_API int pq_code_bits(pq_quant_t q);
