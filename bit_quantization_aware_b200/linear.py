@@ -9,6 +9,15 @@ dWq = dy^T x, which the quantizer's backward takes (``pq_fakequant_bwd``,
 Wq in 128 x 128 tiles with its transpose) and runs the products on the tensor
 cores (``pq.pq_fp8_gemm``). It holds the codes between forward and backward
 and allocates nothing but the outputs that the caller leaves out.
+
+Every operand is rounded to e4m3 (three mantissa bits) on the way, Wq among
+them: the products are those of the codes, x' W'^T and so on, not of Wq to the
+bit. A row's levels are multiples of its own alpha while a tile has one scale
+for 128 rows, so the levels fall between codes: of normal weights with the
+quantizers' initial alphas, W' is 2.0 to 2.7% from Wq (root mean square;
+single weights up to 5.9%, never more than 2^-4), and the packed codes do not
+hold W'. Where the weights that are served have to be multiplied as they are,
+take a bf16 product of Wq or ``pq_wq_gemm`` of the packed codes.
 """
 from __future__ import annotations
 
@@ -48,7 +57,8 @@ class _Operand:
 
 class Fp8Linear:
     """One linear layer of ``out_features`` x ``in_features`` weights over up
-    to ``max_tokens`` tokens a step."""
+    to ``max_tokens`` tokens a step, its operands rounded to e4m3 (how far
+    that is from x Wq^T: see the module)."""
 
     def __init__(self, out_features, in_features, max_tokens, device="cuda"):
         if min(out_features, in_features, max_tokens) < 1:
@@ -69,8 +79,9 @@ class Fp8Linear:
         return pq._new(like, (rows, cols), torch.bfloat16, stream)
 
     def forward(self, x, wq, y_out=None, stream=None):
-        """y = x Wq^T (bf16 [tokens, out_features], or ``y_out``'s type) from x
-        [tokens, in_features] and wq [out_features, in_features]."""
+        """y = x Wq^T of the operands' e4m3 codes (bf16 [tokens,
+        out_features], or ``y_out``'s type) from x [tokens, in_features] and
+        wq [out_features, in_features]."""
         m = x.shape[0]
         if not 1 <= m <= self.max_tokens:
             raise ValueError(f"Fp8Linear: 1 to {self.max_tokens} tokens, got {m}")
