@@ -260,6 +260,9 @@ __global__ void __launch_bounds__(kThreads) norm_end_kernel(const NormEnd e) {
     if (threadIdx.x == 0) write_end(e, sum);
 }
 
+// Scaling rounds twice for a 16-bit output: the product to fp32, as the updates
+// that take the factor do, and that to the type. One rounding would need the
+// product's remainder, a second operation an element, for 2^-24 of the value.
 template <typename T, typename O, int CAP>
 struct ScaleBatch {
     BatchT<TensorDesc, CAP> b;

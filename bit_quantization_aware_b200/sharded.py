@@ -312,12 +312,15 @@ class ShardedQuantStep:
         self.lib.pq_reduce_bwd_adamw(self.q, sources, mult, shards, hp_w, hp_alpha, stream, **clip)
 
     def clip_coef(self, max_norm, gather=None, grad_mult=None, stream=None):
-        """(norm, factor), fp32 [1] each, of the whole step's reduced
-        gradients: this rank's shards add their squares, ``gather`` (fp64 [1]
-        of this rank -> fp64 [world] of all, ordered with the stream like the
-        barrier; not needed for one rank) collects the ranks' sums, and every
-        rank adds them in the same order, so all clip alike. Both are this
-        object's buffers, which its next call overwrites."""
+        """(norm, factor), fp32 [1] each, of the reduced gradients of every
+        rank's matrices: this rank's shards add their squares, ``gather``
+        (fp64 [1] of this rank -> fp64 [world] of all, ordered with the stream
+        like the barrier; not needed for one rank) collects the ranks' sums,
+        and every rank adds them in the same order, so all clip alike. A
+        model's other parameters count where ``gather`` puts their sums of
+        squares behind the ranks' (any number, the same on every rank, each
+        parameter once: ``pq.pq_grad_norm``'s ``sumsq_out``). Both results are
+        this object's buffers, which its next call overwrites."""
         if gather is None and self.world > 1:
             raise ValueError("clip_coef needs a gather over the ranks' sums")
         sources, mult, shards = self._reduce_args(grad_mult)
@@ -342,7 +345,8 @@ class ShardedQuantStep:
         upstream gradient into ``g``: wait at ``barrier`` until every
         rank's gradient is written, then reduce + backward + AdamW on the
         owned shards. With ``max_norm`` the gradients are clipped by the
-        global norm first (``gather``: see ``clip_coef``); returns that norm
+        norm over all ranks first (``gather``, and how to count other
+        parameters: see ``clip_coef``); returns that norm
         (fp32 [1]), else None."""
         barrier()
         if max_norm is None:

@@ -149,7 +149,9 @@ class QuantStep:
     def grad_norm(self, max_norm, stream=None):
         """(norm, clipping factor), fp32 [1] each, of the quantizer gradients
         of every matrix, formed from w, alpha and g: the factor is what
-        ``pq_fakequant_bwd_adamw`` takes as ``coef``. The matrices' dW and
+        ``pq_fakequant_bwd_adamw`` takes as ``coef``. A model's other
+        parameters are not in it: ``pq.pq_grad_norm`` takes their tensors
+        beside these matrices. The matrices' dW and
         d(alpha) stay as they are. Both results are this object's buffers,
         which its next call overwrites."""
         ws, norm, coef = self._norm

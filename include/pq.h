@@ -273,8 +273,10 @@ typedef enum {
 } pq_dtype_t;
 
 /* One gradient tensor (device pointers; `numel` consecutive elements). A
- * scaling call writes data[i] * coef, rounded once to the output's type, to
- * `out`, or back to `data` when out is NULL. out_dtype is dtype or PQ_FP32;
+ * scaling call writes data[i] * coef, the product rounded to fp32 and that to
+ * the output's type (so a 16-bit output may be the neighbour of the nearest
+ * value: 2^-24 of the product more than half a step), to `out`, or back to
+ * `data` when out is NULL. out_dtype is dtype or PQ_FP32;
  * out is data itself (same type) or overlaps neither it nor another tensor's
  * data or out. Pointers are aligned to their
  * element; 32-byte aligned tensors take the vector path, others an element
@@ -299,7 +301,8 @@ typedef struct {
  * Squares and sums are fp64 in a fixed order: the range of every type's
  * squares is kept and the same call gives the same bits. An Inf gradient
  * gives norm = Inf and coef = 0 (Inf * 0 = NaN where it is scaled); a NaN
- * makes both NaN. No gradients give norm 0 and coef 1.
+ * makes both NaN. No gradients give norm 0, and coef 1 where max_norm is at
+ * least 1e-6.
  *   max_norm     >= 0; infinity gives coef 1 for every finite norm (and NaN for
  *                an infinite one)
  *   every pointer is aligned to its element, else PQ_ERR_MISALIGNED

@@ -75,3 +75,14 @@ def test_clipping_without_outputs_is_refused(pq):
         st.clip_grads(1.0)
     st.grad_norm(1.0)  # which needs none
     assert len(pq.calls) == 1
+
+
+def test_other_parameters_count_through_gather():
+    """Sums behind the ranks' enter the norm and the factor."""
+    mats = [I.Matrix("a", 16, 64, 0, 0)]
+    st = ShardedQuantStep(mats, 3, 0, 1, LocalPeers(1), device="cpu", lib=ClipLib)
+    st.g(0).fill_(0.5)  # 256 in squares
+    other = torch.tensor([900.0, 69.0], dtype=torch.float64)
+    norm = st.backward(lambda: None, None, None, max_norm=7.0, gather=lambda mine: torch.cat([mine, other]))
+    assert float(norm) == 35.0
+    assert torch.allclose(st.w_shard(0), torch.full((16, 64), 0.5 * 7 / 35), rtol=2.0 ** -22, atol=0)
