@@ -236,8 +236,7 @@ __device__ __forceinline__ bool mbar_try_warp(uint32_t mbar, uint32_t parity) {
     return __all_sync(0xFFFFFFFFu, done);
 }
 
-// The same asked ahead: the answer takes some 100 to 200 cycles, in which the
-// warp does other work.
+// The same asked ahead: the warp does other work while the answer is on its way.
 __device__ __forceinline__ uint32_t mbar_test(uint32_t mbar, uint32_t parity) {
     uint32_t done;
     asm volatile(
@@ -250,9 +249,9 @@ __device__ __forceinline__ uint32_t mbar_test(uint32_t mbar, uint32_t parity) {
     return done;
 }
 
-// Bounded wait of a whole warp, which stays converged and uniform. A round
-// trip between two warps over two such waits measured 175 cycles, one lane's
-// wait with a shuffle of its result 425.
+// Bounded wait of a whole warp, which stays converged and uniform: a round trip
+// between two warps was shorter so than with one lane's wait and a shuffle of
+// its result.
 template <int HEARD = kCta>
 __device__ __forceinline__ bool uniform_wait(uint32_t mbar, uint32_t parity, volatile int* abort) {
     for (uint32_t i = 0; i < kMaxSpins; ++i) {
@@ -325,9 +324,9 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
 
 // acc += s * (v * b) on pairs of neighbours, b left out where it is 1. Two
 // values an instruction: the promote warps' arithmetic fills the issue slots
-// that the issuers' instructions wait for (8192 x 14336 x 4096: 476 us with
-// one value an instruction, 446 with two; row scales, 4096 x 4096 x 8190: 330
-// and 255), although alone, behind TMEM reads, one at a time is faster.
+// that the issuers' instructions wait for (8192 x 14336 x 4096, cold, when this
+// came: 476 us with one value an instruction, 446 with two; row scales,
+// 4096 x 4096 x 8190: 330 and 255).
 __device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
     uint64_t v;
     asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
@@ -396,9 +395,8 @@ __device__ __forceinline__ void tile_of(const Params& p, int t, int& tm, int& tn
 // by the TMA engine, or, where y does not suit it, row by row. The engine clips
 // rows beyond y, but columns only to a multiple of 16 bytes: with n = 198 it
 // wrote columns 198 and 199 of a wider matrix, so an end inside 16 bytes goes
-// row by row, too. Direct stores of whole sectors of each thread's row took
-// 5000 cycles a tile, during which no K block left TMEM; element by element
-// (an odd pitch) they made up most of a small product's time.
+// row by row, too. No K block leaves TMEM during the stores, and direct ones of
+// each thread's row, whole sectors or (an odd pitch) elements, took longer.
 template <typename T, int C, bool ROWS>
 __device__ __forceinline__ void store_typed(const Params& p, uint32_t buf, int lane, int64_t row0, int64_t col,
                                             const float (&acc)[C]) {
@@ -630,9 +628,8 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
         } else if (warp == 1 || (L::kParts == 2 && warp == 3 && rank == 0)) {
             if (!PAIR || rank == 0) {
                 // ------------------------------------------------ MMA issuer
-                // The whole warp walks the loop and one lane issues: the
-                // descriptors then stay in uniform registers. Inside a branch
-                // of one lane each MMA took some 95 cycles to issue.
+                // The whole warp walks the loop and one lane issues, which
+                // was faster than a branch of one lane around the loop.
                 constexpr uint32_t idesc = idesc_e4m3(kTileRows, L::kCols);
                 const int h = warp == 3;
                 const uint32_t dfull = b_dfull + 8u * L::kBufs * h, dempty = b_dempty + 8u * L::kBufs * h;
@@ -640,10 +637,9 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
                 StageRing r(p.stages);
                 Ring<L::kBufs> d;
                 bool ok = true;
-                // Three waits one after the other took most of a K block's
-                // time, so the next block's are asked for before this one's
-                // MMAs (512 x 4096 x 4096: 15.9 -> 15.2 us). A pair's two
-                // issuers have the time: asking ahead cost them 2%.
+                // The next block's waits are asked for before this one's
+                // MMAs (512 x 4096 x 4096, when this came: 15.9 -> 15.2 us). A
+                // pair's two issuers have the time: asking ahead cost them 2%.
                 constexpr bool kAhead = L::kParts == 1;
                 uint32_t ready = 0;
                 for (int t = first; ok && t < tiles; t += step) {
@@ -743,7 +739,7 @@ __global__ void __cluster_dims__(Layout<NT, BROW, SPLIT, PAIR>::kCluster, 1, 1)
         auto sum_blocks_tile = [&](float(&acc)[C], int64_t row, int64_t col) -> bool {
             constexpr int W = NT == 64 ? 16 : 32;  // columns of a read (registers)
             // rows, columns and K blocks beyond the last take the last one's
-            // scale (a branch around each load took 60 cycles)
+            // scale: no branch around the loads
             const float* sa = p.sa + (row < p.m ? row : p.m - 1);
             const float* sb = p.sb + (col < p.n ? col / kBlock : (p.n - 1) / kBlock) * p.kb;
             // scales four K blocks at a time, the next four on their way; an
@@ -1034,14 +1030,17 @@ static int64_t clusters_resident() {
 
 // Tile width and K split of a problem: the least estimated time
 //   4 + waves * (K blocks of a CTA * time of one + 1 + exchange) microseconds
-// among the kernels. The times of a K block fit what they measured, tile
-// scales / row scales: pairs 0.5 / 0.85 (8192 x 14336 x 4096: 449 us;
-// 4096 x 4096 x 8190 by rows: 209), 128 wide 0.28 (512 x 4096 x 4096: 14.0, in
+// among the kernels. The times of a K block fit what they measured cold when
+// they were built, tile scales / row scales: pairs 0.5 / 0.85
+// (8192 x 14336 x 4096: 449 us; 4096 x 4096 x 8190 by rows: 209), 128 wide 0.28 (512 x 4096 x 4096: 14.0, in
 // pairs 19.6; with row scales 0.6, so that 64 wide, of which two share an SM,
 // is always ahead, and there is no such kernel), 64 wide 0.24 / 0.45, or 0.36 / 0.55 where two CTAs
 // share an SM (77 x 14336 x 4096: 17.0, 128 wide 14.7). The exchange of a
 // split grows with the sums that it moves: 1 x 4096 x 4096 took 13.5 us in
 // one piece, 10.6 by 2 and 8.0 by 4; 300 x 700 x 2000 (64 wide) 9.7, 8.0 and 7.9.
+// Every kernel forced in turn on 27 products of the layers' sizes, decode to
+// training batches, split and not: the choice was the fastest at 26 and 1% off
+// at one (77 x 4096 x 14336).
 struct Plan {
     int nt, split;
     bool pair;
