@@ -392,10 +392,8 @@ __device__ __forceinline__ void tile_of(const Params& p, int t, int& tm, int& tn
 // A warp's 32 rows x C columns to y by way of its 4 KB of shared memory, 128
 // bytes of each row at a time (the 128B swizzle: 16-byte chunk c of row r at
 // chunk c ^ (r % 8), so the writes are free of bank conflicts), and from there
-// by the TMA engine, or, where y does not suit it, row by row. The engine clips
-// rows beyond y, but columns only to a multiple of 16 bytes: with n = 198 it
-// wrote columns 198 and 199 of a wider matrix, so an end inside 16 bytes goes
-// row by row, too. No K block leaves TMEM during the stores, and direct ones of
+// by the TMA engine, which clips what lies beyond y, or, where y does not suit
+// it, row by row. No K block leaves TMEM during the stores, and direct ones of
 // each thread's row, whole sectors or (an odd pitch) elements, took longer.
 template <typename T, int C, bool ROWS>
 __device__ __forceinline__ void store_typed(const Params& p, uint32_t buf, int lane, int64_t row0, int64_t col,
@@ -435,7 +433,7 @@ __device__ __forceinline__ void store_typed(const Params& p, uint32_t buf, int l
                              : "memory");
             }
         }
-        if (p.tma_out && (col + c + W <= p.n || p.n % (16 / B) == 0)) {
+        if (p.tma_out) {
             fence_async_smem();
             __syncwarp();
             if (lane == 0 && row0 < p.m && col + c < p.n) {
@@ -1115,9 +1113,14 @@ static pq_status_t launch(Params& p, const uint8_t* a, int64_t lda, const uint8_
     if (!enc || !encode(enc, &p.ta, kByte, 1, a, p.m, k, lda, a_rows) ||
         !encode(enc, &p.tb, kByte, 1, b, p.n, k, ldb, L::kBRows))
         return PQ_ERR_CUDA;
-    // TMA stores want 16-byte aligned rows, less than 2^40 bytes apart
+    // TMA stores want 16-byte aligned rows, less than 2^40 bytes apart, that end
+    // on 16 bytes, too: columns are clipped to a multiple of 16 bytes only (with
+    // n = 198 in rows of 200, columns 198 and 199 were written). Deciding it in
+    // the kernel, for the last tile alone, cost every large product 10 to 17%:
+    // the registers of its sums.
     const int size = bytes_of(p.dtype);
-    p.tma_out = SPLIT == 1 && pq::aligned(p.y, 16) && p.ldy < (int64_t{1} << 40) / size && p.ldy * size % 16 == 0;
+    p.tma_out = SPLIT == 1 && pq::aligned(p.y, 16) && p.ldy < (int64_t{1} << 40) / size && p.ldy * size % 16 == 0 &&
+                p.n * size % 16 == 0;
     if (p.tma_out && !encode(enc, &p.ty, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
                              size, p.y, p.m, p.n, p.ldy, 32))
         return PQ_ERR_CUDA;
