@@ -1030,15 +1030,16 @@ static int64_t clusters_resident() {
 //   4 + waves * (K blocks of a CTA * time of one + 1 + exchange) microseconds
 // among the kernels. The times of a K block fit what they measured cold when
 // they were built, tile scales / row scales: pairs 0.5 / 0.85
-// (8192 x 14336 x 4096: 449 us; 4096 x 4096 x 8190 by rows: 209), 128 wide 0.28 (512 x 4096 x 4096: 14.0, in
-// pairs 19.6; with row scales 0.6, so that 64 wide, of which two share an SM,
-// is always ahead, and there is no such kernel), 64 wide 0.24 / 0.45, or 0.36 / 0.55 where two CTAs
-// share an SM (77 x 14336 x 4096: 17.0, 128 wide 14.7). The exchange of a
-// split grows with the sums that it moves: 1 x 4096 x 4096 took 13.5 us in
-// one piece, 10.6 by 2 and 8.0 by 4; 300 x 700 x 2000 (64 wide) 9.7, 8.0 and 7.9.
-// Every kernel forced in turn on 27 products of the layers' sizes, decode to
-// training batches, split and not: the choice was the fastest at 26 and 1% off
-// at one (77 x 4096 x 14336).
+// (8192 x 14336 x 4096: 449 us; 4096 x 4096 x 8190 by rows: 209), 128 wide 0.28
+// (512 x 4096 x 4096: 14.0, in pairs 19.6; with row scales 0.6, so that 64
+// wide, of which two share an SM, is always ahead, and there is no such
+// kernel), 64 wide 0.24 / 0.45, or 0.36 / 0.55 where two CTAs share an SM
+// (77 x 14336 x 4096: 17.0, 128 wide 14.7). The exchange of a split grows with
+// the sums that it moves: 1 x 4096 x 4096 took 13.5 us in one piece, 10.6 by 2
+// and 8.0 by 4; 300 x 700 x 2000 (64 wide) 9.7, 8.0 and 7.9. With every kernel
+// forced in turn on 27 products of layers' sizes, from one token to training
+// batches, the choice was the fastest, or within 1% of it, at 26 and 2% off at
+// one (77 x 4096 x 14336).
 struct Plan {
     int nt, split;
     bool pair;
